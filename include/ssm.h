@@ -15,6 +15,13 @@
  *   ssm_gated_rmsnorm_fwd  the Mamba-2 mixer's gated RMS norm after the SSD.
  *   ssd_attention_fwd   the SSD map's hidden attention matrix, per head.
  *
+ * and the mixer of the gated delta rule, next to the SSD's:
+ *
+ *   gdr_chunk_scan_fwd  the gated delta rule over prompts, dense or packed.
+ *   gdr_scan_step       one decode token against a cache of its states.
+ *   gdr_gated_rmsnorm_fwd  its norm: RMS per head, then the gate.
+ *   ssm_conv1d_packed_fwd  the causal convolution over packed sequences.
+ *
  * Conventions for every call
  * --------------------------
  * - Pointers are DEVICE pointers (cudaMalloc'd or otherwise device-visible),
@@ -466,6 +473,160 @@ typedef struct ssd_attention_args {
 
 ssm_status_t ssd_attention_workspace(const ssd_attention_args_t *args, size_t *bytes);
 ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * gdr_chunk_scan_fwd -- the gated delta rule over prompts.
+ *
+ * The scan of a linear-attention mixer with a K x V state matrix per head,
+ * whose write first takes out what the state already holds for the key
+ * (the delta rule), after a scalar decay per head and token (the gate).
+ * For sequence i, value head h (key head g = h / (heads / key_heads)) and
+ * token t:
+ *
+ *   a     = exp(d * A[h]),  d = softplus(dt[t,h] + dt_bias[h])
+ *                           (flag SSM_DT_SOFTPLUS, else dt + dt_bias)
+ *   b     = sigmoid(beta[t,h])   (flag GDR_BETA_SIGMOID, else beta)
+ *   k, q  = k[t,g,:] / sqrt(|k|^2 + l2_eps), q likewise
+ *                           (flag GDR_QK_L2NORM, else as they are)
+ *   u[v]  = b * (v[t,h,v] - a * sum_k k[k] * S[k,v])
+ *   S     = a * S + outer(k, u)                               (K x V)
+ *   y[v]  = scale * sum_k q[k] * S[k,v]
+ *
+ * with S starting from the sequence's state (zeros if h0 == NULL); y_t reads
+ * the state after token t's write.  dt == NULL: no decay (a = 1; A and
+ * dt_bias are not read).
+ *
+ *   q, k   : [batch, seqlen, key_heads, key_dim]    io type
+ *   v      : [batch, seqlen, heads, value_dim]      io type
+ *   dt, beta : [batch, seqlen, heads]               io type; dt may be NULL
+ *   A      : [heads] float32, <= 0 (pass -exp(A_log)); dt_bias: [heads] or NULL (= 0)
+ *   y      : [batch, seqlen, heads, value_dim]      io type, dense
+ *   q_row, k_row, v_row, dt_row, beta_row: elements from one token's row to
+ *            the next, 0 = dense.  A token's heads are dense; batch rows are
+ *            seqlen rows apart.  So slices of one wider projection go in as
+ *            they lie.  dt and beta need no 16-byte alignment.
+ *   cu_seqlens : [sequences + 1] int32 device memory, or NULL.  When given,
+ *            batch must be 1 and the sequences lie one behind the other:
+ *            sequence i is the tokens cu_seqlens[i] .. cu_seqlens[i + 1] of
+ *            the seqlen rows.  Rows that belong to no sequence are not read
+ *            and their y rows are left as they were.  A pair that is out of
+ *            order or outside 0 .. seqlen is taken as an empty sequence.
+ *            When NULL the sequences are the batch rows (`sequences` = batch).
+ *   h0, h_last : [state_rows, heads, key_dim, value_dim] float32 (key side
+ *            first) or NULL; h_last may equal h0 (states updated in place).
+ *   slots  : [sequences] int32 device memory, or NULL: the row of h0 and
+ *            h_last that is sequence i's state (NULL: row i).  A sequence
+ *            whose slot is outside 0 .. state_rows - 1 is skipped: nothing of it
+ *            is read or written.  Slots in use must differ (two sequences in
+ *            one slot race on it).
+ *   An empty sequence copies its state from h0 (or zeros) to h_last.
+ *   workspace: gdr_chunk_scan_workspace() bytes, or NULL if that is 0.  Word 0
+ *            is the call's status word, as for ssm_scan_fwd.
+ *
+ * bf16 with key_dim <= 128 runs on the tensor cores, 64 tokens a chunk; a
+ * value that is not finite then also reaches earlier tokens of its chunk.
+ * Everything else runs token by token in float32.  key_dim 1..256.
+ * ---------------------------------------------------------------------- */
+#define GDR_BETA_SIGMOID 8u
+#define GDR_QK_L2NORM 16u
+
+typedef struct gdr_scan_args {
+  int64_t batch, seqlen, heads, key_heads, key_dim, value_dim;
+  int64_t sequences, state_rows;
+  int64_t q_row, k_row, v_row, dt_row, beta_row;
+  int32_t io;
+  uint32_t flags;
+  float scale, l2_eps;
+  const void *q, *k, *v, *dt, *beta;
+  const float *A, *dt_bias, *h0;
+  const int32_t *cu_seqlens, *slots;
+  void *y;
+  float *h_last;
+  void *workspace;
+  size_t workspace_bytes;
+} gdr_scan_args_t;
+
+ssm_status_t gdr_chunk_scan_workspace(const gdr_scan_args_t *args, size_t *bytes);
+ssm_status_t gdr_chunk_scan_fwd(const gdr_scan_args_t *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * gdr_scan_step -- one decode token per sequence, states updated in place.
+ *
+ * The arithmetic is one token of gdr_chunk_scan_fwd, in float32.
+ *   q, k: [batch, key_heads, key_dim]; v, y: [batch, heads, value_dim];
+ *   dt, beta: [batch, heads]; *_row: elements between batch rows (0 = dense);
+ *   state: [state_rows, heads, key_dim, value_dim] float32;
+ *   slots: [batch] int32 device memory or NULL (row i uses state i).  A row
+ *   whose slot is outside 0 .. state_rows - 1 (the padding of a captured
+ *   batch) is skipped and its y row left as it was.  Slots in use must differ.
+ * ---------------------------------------------------------------------- */
+typedef struct gdr_step_args {
+  int64_t batch, heads, key_heads, key_dim, value_dim, state_rows;
+  int64_t q_row, k_row, v_row, dt_row, beta_row;
+  int32_t io;
+  uint32_t flags;
+  float scale, l2_eps;
+  const void *q, *k, *v, *dt, *beta;
+  const float *A, *dt_bias;
+  const int32_t *slots;
+  float *state_io;
+  void *y;
+} gdr_step_args_t;
+
+ssm_status_t gdr_scan_step(const gdr_step_args_t *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * gdr_gated_rmsnorm_fwd -- the gated delta rule's norm, after the scan.
+ *
+ * Per token and head (ssm_gated_rmsnorm_fwd gates first and normalises over
+ * the whole width):
+ *
+ *   out = x / sqrt(mean(x^2) + eps) * weight * silu(z)
+ *
+ *   x, out: [tokens, heads, width] (io), dense; z: the same shape, `z_row`
+ *   elements between tokens (0 = dense), or NULL (no gate); weight: [width]
+ *   float32 or NULL (ones).  out may be x, nothing else may overlap it.
+ * width 1..8192.  bf16 uses silu = z (1 + tanh(z/2)) / 2 with the hardware
+ * tanh; float32 uses z / (1 + exp(-z)).
+ * ---------------------------------------------------------------------- */
+typedef struct gdr_norm_args {
+  int64_t tokens, heads, width, z_row;
+  int32_t io;
+  uint32_t flags; /* 0 */
+  float eps;
+  const void *x, *z;
+  const float *weight;
+  void *out;
+} gdr_norm_args_t;
+
+ssm_status_t gdr_gated_rmsnorm_fwd(const gdr_norm_args_t *args, void *stream);
+
+/* ------------------------------------------------------------------------
+ * ssm_conv1d_packed_fwd -- ssm_conv1d_fwd over packed sequences.
+ *
+ * x, u: [tokens, channels] (io), `x_row` elements between x's rows (0 =
+ * dense), u dense; w, bias, flags and the arithmetic as ssm_conv1d_fwd.
+ *   cu_seqlens: [sequences + 1] int32, non-decreasing: sequence i is the rows
+ *     cu_seqlens[i] .. cu_seqlens[i + 1].  Rows of no sequence are left as
+ *     they were.  A pair outside 0 .. tokens is an empty sequence.
+ *   state: [state_rows, channels, width - 1] float32 or NULL (zeros): the
+ *     inputs before each sequence, oldest first, updated in place to the
+ *     last width - 1 inputs (a decode batch is sequences of one token).
+ *   slots: [sequences] int32 or NULL, as for gdr_chunk_scan_fwd (a sequence
+ *     whose slot is out of range is skipped).
+ * ---------------------------------------------------------------------- */
+typedef struct ssm_conv_packed_args {
+  int64_t tokens, channels, width, sequences, state_rows, x_row;
+  int32_t io;
+  uint32_t flags;
+  const void *x;
+  const float *w, *bias;
+  float *state_io;
+  const int32_t *cu_seqlens, *slots;
+  void *u;
+} ssm_conv_packed_args_t;
+
+ssm_status_t ssm_conv1d_packed_fwd(const ssm_conv_packed_args_t *args, void *stream);
 
 /* A short English description of a status; never NULL. */
 const char *ssm_status_string(ssm_status_t status);

@@ -20,6 +20,7 @@ STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULL", 2: "SSM_ERR_SHAPE", 3: "SSM_ERR_DTYPE"
           7: "SSM_ERR_CUDA", 8: "SSM_ERR_TIMEOUT"}
 
 SSM_CONV_SILU = 1
+GDR_BETA_SIGMOID, GDR_QK_L2NORM = 8, 16
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -86,6 +87,45 @@ class AttnArgs(ctypes.Structure):
                 ("alpha", _vp), ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class GdrScanArgs(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("heads", _i64), ("key_heads", _i64),
+                ("key_dim", _i64), ("value_dim", _i64), ("sequences", _i64),
+                ("state_rows", _i64),
+                ("q_row", _i64), ("k_row", _i64), ("v_row", _i64), ("dt_row", _i64),
+                ("beta_row", _i64),
+                ("io", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("l2_eps", ctypes.c_float),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("dt", _vp), ("beta", _vp),
+                ("A", _vp), ("dt_bias", _vp), ("h0", _vp), ("cu_seqlens", _vp), ("slots", _vp),
+                ("y", _vp), ("h_last", _vp),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GdrStepArgs(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("heads", _i64), ("key_heads", _i64), ("key_dim", _i64),
+                ("value_dim", _i64), ("state_rows", _i64),
+                ("q_row", _i64), ("k_row", _i64), ("v_row", _i64), ("dt_row", _i64),
+                ("beta_row", _i64),
+                ("io", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("scale", ctypes.c_float), ("l2_eps", ctypes.c_float),
+                ("q", _vp), ("k", _vp), ("v", _vp), ("dt", _vp), ("beta", _vp),
+                ("A", _vp), ("dt_bias", _vp), ("slots", _vp), ("state_io", _vp), ("y", _vp)]
+
+
+class GdrNormArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("heads", _i64), ("width", _i64), ("z_row", _i64),
+                ("io", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("x", _vp), ("z", _vp), ("weight", _vp), ("out", _vp)]
+
+
+class ConvPackedArgs(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("channels", _i64), ("width", _i64), ("sequences", _i64),
+                ("state_rows", _i64), ("x_row", _i64),
+                ("io", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("x", _vp), ("w", _vp), ("bias", _vp), ("state_io", _vp), ("cu_seqlens", _vp),
+                ("slots", _vp), ("u", _vp)]
+
+
 def header_functions(path=HEADER):
     """Names of the functions include/ssm.h declares."""
     with open(path) as f:
@@ -126,6 +166,15 @@ def lib():
         L.ssm_scan_fwd_host.argtypes = [ctypes.POINTER(ScanArgs), _vp]
         L.ssm_scan_host_workspace.argtypes = [ctypes.POINTER(ScanArgs),
                                               ctypes.POINTER(ctypes.c_size_t)]
+        L.gdr_chunk_scan_fwd.argtypes = [ctypes.POINTER(GdrScanArgs), _vp]
+        L.gdr_chunk_scan_workspace.argtypes = [ctypes.POINTER(GdrScanArgs),
+                                               ctypes.POINTER(ctypes.c_size_t)]
+        L.gdr_scan_step.argtypes = [ctypes.POINTER(GdrStepArgs), _vp]
+        L.gdr_gated_rmsnorm_fwd.argtypes = [ctypes.POINTER(GdrNormArgs), _vp]
+        L.ssm_conv1d_packed_fwd.argtypes = [ctypes.POINTER(ConvPackedArgs), _vp]
+        for fn in (L.gdr_chunk_scan_fwd, L.gdr_chunk_scan_workspace, L.gdr_scan_step,
+                   L.gdr_gated_rmsnorm_fwd, L.ssm_conv1d_packed_fwd):
+            fn.restype = ctypes.c_int
         for fn in (L.ssm_scan_fwd_static, L.ssm_workspace_status, L.ssm_scan_fwd_host,
                    L.ssm_scan_host_workspace,
                    L.ssm_scan_fwd, L.ssm_scan_workspace, L.ssd_chunk_scan_fwd,

@@ -1,0 +1,260 @@
+// gdr_api.cu -- the exported C ABI of the gated delta rule's operators
+// (include/ssm.h): argument validation on the host, then dispatch.  Nothing
+// is launched when a check fails, and nothing here allocates memory.
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ssm.h"
+
+namespace {
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+template <typename... Ps>
+bool all_aligned(uintptr_t to, Ps... ps) {
+  const void *arr[] = {static_cast<const void *>(ps)...};
+  for (const void *p : arr)
+    if (!aligned(p, to)) return false;
+  return true;
+}
+
+bool overlap(const void *p, size_t np, const void *q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && np && nq && a < b + nq && b < a + np;
+}
+
+ssm_status_t from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return SSM_OK;
+  if (e == cudaErrorNotSupported) return SSM_ERR_UNSUPPORTED;
+  return SSM_ERR_CUDA;
+}
+
+// Sizes below kMaxSize, and tensors of at most kMaxValues values (far beyond
+// a GPU's memory), keep every product the checks and kernels form in 64 bits.
+constexpr int64_t kMaxSize = 1ll << 31;
+constexpr double kMaxValues = 1e15;
+
+// What the prompt scan and the step share: sizes, flags and dtype.
+template <typename Args>
+ssm_status_t check_heads(const Args *a) {
+  if (a->io != SSM_F32 && a->io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (a->batch < 0 || a->heads <= 0 || a->key_heads <= 0 || a->heads % a->key_heads ||
+      a->key_dim <= 0 || a->value_dim <= 0 || a->state_rows < 0)
+    return SSM_ERR_SHAPE;
+  if (a->flags & ~(SSM_DT_SOFTPLUS | GDR_BETA_SIGMOID | GDR_QK_L2NORM)) return SSM_ERR_UNSUPPORTED;
+  if (!(fabsf(a->scale) <= 3.0e38f)) return SSM_ERR_SHAPE;
+  if ((a->flags & GDR_QK_L2NORM) && !(a->l2_eps >= 0.f && a->l2_eps <= 3.0e38f)) return SSM_ERR_SHAPE;
+  if (a->key_dim > ssm::kGdrMaxKeyDim || a->value_dim > 65536 || a->heads > 65535 ||
+      a->batch >= kMaxSize || a->state_rows >= kMaxSize ||
+      (double)a->state_rows * a->heads * a->key_dim * a->value_dim > kMaxValues)
+    return SSM_ERR_UNSUPPORTED;
+  // a row stride is 0 (dense) or at least the row itself
+  const int64_t kr = a->key_heads * a->key_dim, vr = a->heads * a->value_dim;
+  if ((a->q_row && a->q_row < kr) || (a->k_row && a->k_row < kr) || (a->v_row && a->v_row < vr) ||
+      (a->dt_row && a->dt_row < a->heads) || (a->beta_row && a->beta_row < a->heads))
+    return SSM_ERR_SHAPE;
+  if (a->q_row >= kMaxSize || a->k_row >= kMaxSize || a->v_row >= kMaxSize ||
+      a->dt_row >= kMaxSize || a->beta_row >= kMaxSize)
+    return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+// y must not overlap an input of `rows` rows.
+template <typename Args>
+bool y_overlaps(const Args *a, int64_t rows) {
+  const size_t es = a->io == SSM_BF16 ? 2 : 4;
+  auto bytes = [&](int64_t row, int64_t width) {
+    return rows > 0 ? (size_t)((rows - 1) * (row ? row : width) + width) * es : (size_t)0;
+  };
+  const int64_t kr = a->key_heads * a->key_dim, vr = a->heads * a->value_dim;
+  const size_t yb = bytes(0, vr);
+  return overlap(a->y, yb, a->q, bytes(a->q_row, kr)) || overlap(a->y, yb, a->k, bytes(a->k_row, kr)) ||
+         overlap(a->y, yb, a->v, bytes(a->v_row, vr)) ||
+         overlap(a->y, yb, a->dt, bytes(a->dt_row, a->heads)) ||
+         overlap(a->y, yb, a->beta, bytes(a->beta_row, a->heads));
+}
+
+template <typename Args>
+void fill_heads(ssm::GdrParams &p, const Args *a) {
+  p.H = a->heads;
+  p.Hk = a->key_heads;
+  p.K = a->key_dim;
+  p.V = a->value_dim;
+  p.state_rows = a->state_rows;
+  p.q_row = a->q_row ? a->q_row : a->key_heads * a->key_dim;
+  p.k_row = a->k_row ? a->k_row : a->key_heads * a->key_dim;
+  p.v_row = a->v_row ? a->v_row : a->heads * a->value_dim;
+  p.dt_row = a->dt_row ? a->dt_row : a->heads;
+  p.beta_row = a->beta_row ? a->beta_row : a->heads;
+  p.flags = a->flags;
+  p.io = a->io;
+  p.scale = a->scale;
+  p.l2_eps = a->l2_eps;
+  p.q = a->q;
+  p.k = a->k;
+  p.v = a->v;
+  p.dt = a->dt;
+  p.beta = a->beta;
+  p.A = a->A;
+  p.dt_bias = a->dt_bias;
+  p.slots = a->slots;
+  p.y = a->y;
+}
+
+ssm_status_t check_gdr(const gdr_scan_args_t *a, bool shapes_only) {
+  if (!a) return SSM_ERR_NULL;
+  ssm_status_t st = check_heads(a);
+  if (st != SSM_OK) return st;
+  if (a->seqlen < 0 || a->sequences < 0) return SSM_ERR_SHAPE;
+  if (a->seqlen >= kMaxSize || a->sequences >= kMaxSize ||
+      (a->batch > 0 && a->seqlen > 0 && a->batch >= kMaxSize / a->seqlen) ||
+      (double)a->batch * a->seqlen * a->heads * a->value_dim > kMaxValues)
+    return SSM_ERR_UNSUPPORTED;
+  if (shapes_only) return SSM_OK;
+  if (a->cu_seqlens ? a->batch != 1 : a->sequences != a->batch) return SSM_ERR_SHAPE;
+  if (!a->slots && (a->h0 || a->h_last) && a->state_rows < a->sequences) return SSM_ERR_SHAPE;
+  const int64_t rows = a->batch * a->seqlen;
+  if (a->sequences > 0 && rows > 0 &&
+      (!a->q || !a->k || !a->v || !a->beta || (a->dt && !a->A) || !a->y))
+    return SSM_ERR_NULL;
+  if (!all_aligned(16, a->q, a->k, a->v, a->A, a->dt_bias, a->h0, a->y, a->h_last, a->workspace) ||
+      !all_aligned(a->io == SSM_BF16 ? 2 : 4, a->dt, a->beta) ||
+      !all_aligned(4, a->cu_seqlens, a->slots))
+    return SSM_ERR_ALIGN;
+  if (y_overlaps(a, rows)) return SSM_ERR_SHAPE;
+  const size_t sb = (size_t)(a->state_rows * a->heads) * (size_t)(a->key_dim * a->value_dim) * 4;
+  if (a->h0 != a->h_last && overlap(a->h0, sb, a->h_last, sb)) return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssm_status_t gdr_chunk_scan_workspace(const gdr_scan_args_t *a, size_t *bytes) {
+  if (!bytes) return SSM_ERR_NULL;
+  ssm_status_t st = check_gdr(a, true);
+  if (st != SSM_OK) return st;
+  *bytes = 0;
+  return SSM_OK;
+}
+
+ssm_status_t gdr_chunk_scan_fwd(const gdr_scan_args_t *a, void *stream) {
+  ssm_status_t st = check_gdr(a, false);
+  if (st != SSM_OK) return st;
+  if (a->sequences == 0) return SSM_OK;  // nothing to do, nothing launched
+  ssm::GdrParams p;
+  fill_heads(p, a);
+  p.nseq = a->sequences;
+  p.L = a->seqlen;
+  p.rows = a->batch * a->seqlen;
+  p.h0 = a->h0;
+  p.h_last = a->h_last;
+  p.cu = a->cu_seqlens;
+  return from_cuda(ssm::launch_gdr_recurrent(p, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t gdr_scan_step(const gdr_step_args_t *a, void *stream) {
+  if (!a) return SSM_ERR_NULL;
+  ssm_status_t st = check_heads(a);
+  if (st != SSM_OK) return st;
+  if (a->batch > 0 && (!a->q || !a->k || !a->v || !a->beta || (a->dt && !a->A) || !a->state_io || !a->y))
+    return SSM_ERR_NULL;
+  if ((double)a->batch * a->heads * a->value_dim > kMaxValues) return SSM_ERR_UNSUPPORTED;
+  if (!a->slots && a->state_rows < a->batch) return SSM_ERR_SHAPE;
+  if (!all_aligned(16, a->q, a->k, a->v, a->A, a->dt_bias, a->state_io, a->y) ||
+      !all_aligned(a->io == SSM_BF16 ? 2 : 4, a->dt, a->beta) || !all_aligned(4, a->slots))
+    return SSM_ERR_ALIGN;
+  if (y_overlaps(a, a->batch)) return SSM_ERR_SHAPE;
+  if (a->batch == 0) return SSM_OK;
+  ssm::GdrParams p;
+  fill_heads(p, a);
+  p.nseq = a->batch;
+  p.L = 1;
+  p.rows = a->batch;
+  p.h0 = p.h_last = a->state_io;
+  p.cu = nullptr;
+  return from_cuda(ssm::launch_gdr_step(p, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t gdr_gated_rmsnorm_fwd(const gdr_norm_args_t *a, void *stream) {
+  if (!a) return SSM_ERR_NULL;
+  if (a->io != SSM_F32 && a->io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (a->tokens < 0 || a->heads <= 0 || a->width <= 0 || !(a->eps >= 0.f) || a->eps > 3.0e38f)
+    return SSM_ERR_SHAPE;
+  if (a->flags || a->width > ssm::kHeadNormMaxWidth || a->tokens >= kMaxSize || a->heads > 65535 ||
+      a->z_row >= kMaxSize)
+    return SSM_ERR_UNSUPPORTED;
+  if (a->z_row && a->z_row < a->heads * a->width) return SSM_ERR_SHAPE;
+  if (a->tokens > 0 && (!a->x || !a->out)) return SSM_ERR_NULL;
+  if (!all_aligned(16, a->x, a->z, a->weight, a->out)) return SSM_ERR_ALIGN;
+  const size_t es = a->io == SSM_BF16 ? 2 : 4;
+  const int64_t row = a->heads * a->width, zr = a->z_row ? a->z_row : row;
+  const size_t bytes = (size_t)(a->tokens * row) * es;
+  const size_t zb = a->tokens > 0 ? (size_t)((a->tokens - 1) * zr + row) * es : 0;
+  if (a->out != a->x && overlap(a->out, bytes, a->x, bytes)) return SSM_ERR_SHAPE;
+  if (overlap(a->out, bytes, a->z, zb) ||
+      overlap(a->out, bytes, a->weight, (size_t)a->width * sizeof(float)))
+    return SSM_ERR_SHAPE;
+  if (a->tokens == 0) return SSM_OK;
+  ssm::HeadNormParams p;
+  p.tokens = a->tokens;
+  p.heads = a->heads;
+  p.width = a->width;
+  p.z_row = zr;
+  p.io = a->io;
+  p.eps = a->eps;
+  p.x = a->x;
+  p.z = a->z;
+  p.weight = a->weight;
+  p.out = a->out;
+  return from_cuda(ssm::launch_head_norm(p, static_cast<cudaStream_t>(stream)));
+}
+
+ssm_status_t ssm_conv1d_packed_fwd(const ssm_conv_packed_args_t *a, void *stream) {
+  if (!a) return SSM_ERR_NULL;
+  if (a->io != SSM_F32 && a->io != SSM_BF16) return SSM_ERR_DTYPE;
+  if (a->tokens < 0 || a->channels <= 0 || a->width <= 0 || a->sequences < 0 || a->state_rows < 0)
+    return SSM_ERR_SHAPE;
+  if (a->width > ssm::kConvMaxWidth || (a->flags & ~SSM_CONV_SILU) || a->tokens >= kMaxSize ||
+      a->channels >= (1ll << 24) || a->sequences >= kMaxSize || a->state_rows >= kMaxSize ||
+      a->x_row >= kMaxSize)
+    return SSM_ERR_UNSUPPORTED;
+  if (a->x_row && a->x_row < a->channels) return SSM_ERR_SHAPE;
+  if (!a->w) return SSM_ERR_NULL;
+  const bool work = a->tokens > 0 && a->sequences > 0;
+  if (work && (!a->x || !a->u || !a->cu_seqlens)) return SSM_ERR_NULL;
+  if (a->state_io && !a->slots && a->state_rows < a->sequences) return SSM_ERR_SHAPE;
+  if (!all_aligned(16, a->x, a->u, a->w, a->bias, a->state_io) ||
+      !all_aligned(4, a->cu_seqlens, a->slots))
+    return SSM_ERR_ALIGN;
+  const size_t es = a->io == SSM_BF16 ? 2 : 4;
+  const int64_t xr = a->x_row ? a->x_row : a->channels;
+  const size_t xb = work ? (size_t)((a->tokens - 1) * xr + a->channels) * es : 0;
+  const size_t ub = work ? (size_t)(a->tokens * a->channels) * es : 0;
+  const size_t sb = (size_t)(a->state_rows * a->channels) * (size_t)(a->width - 1) * 4;
+  if (overlap(a->x, xb, a->u, ub) || overlap(a->state_io, sb, a->u, ub) ||
+      overlap(a->state_io, sb, a->x, xb))
+    return SSM_ERR_SHAPE;
+  if (!work) return SSM_OK;
+  ssm::ConvPackedParams p;
+  p.tokens = a->tokens;
+  p.Cc = a->channels;
+  p.nseq = a->sequences;
+  p.state_rows = a->state_rows;
+  p.x_row = xr;
+  p.W = (int)a->width;
+  p.io = a->io;
+  p.silu = (a->flags & SSM_CONV_SILU) != 0;
+  p.x = a->x;
+  p.w = a->w;
+  p.bias = a->bias;
+  p.state = a->width > 1 ? a->state_io : nullptr;
+  p.cu = a->cu_seqlens;
+  p.slots = a->slots;
+  p.u = a->u;
+  return from_cuda(ssm::launch_conv1d_packed(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

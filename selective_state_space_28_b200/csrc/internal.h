@@ -154,6 +154,54 @@ size_t ssd_conv_bc_bytes(int64_t batch, int64_t L, int64_t G);
 cudaError_t launch_ssd_tc(const M2Params &p, int *status, const SsdSplit &split, void *seg_ws,
                           cudaStream_t s, const SsdConv *conv = nullptr);
 
+// The gated delta rule: a prompt scan over batch rows or packed sequences
+// (L rows of tokens in all when cu is set), or its decode step (L = 1).
+// Row strides are in elements and never 0 here.
+struct GdrParams {
+  int64_t nseq, L, rows;  // sequences; tokens of a batch row (dense); rows of q, k, v, y in all
+  int64_t H, Hk, K, V;
+  int64_t state_rows;
+  int64_t q_row, k_row, v_row, dt_row, beta_row;
+  uint32_t flags;
+  int io;
+  float scale, l2_eps;
+  const void *q, *k, *v, *dt, *beta;
+  const float *A, *dt_bias;
+  const float *h0;
+  const int32_t *cu, *slots;
+  void *y;
+  float *h_last;
+};
+constexpr int64_t kGdrMaxKeyDim = 256;
+cudaError_t launch_gdr_recurrent(const GdrParams &p, cudaStream_t s);
+cudaError_t launch_gdr_step(const GdrParams &p, cudaStream_t s);
+
+// RMS norm per head, then the gate.
+constexpr int64_t kHeadNormMaxWidth = 8192;
+struct HeadNormParams {
+  int64_t tokens, heads, width, z_row;
+  int io;
+  float eps;
+  const void *x, *z;
+  const float *weight;
+  void *out;
+};
+cudaError_t launch_head_norm(const HeadNormParams &p, cudaStream_t s);
+
+// The causal convolution over packed sequences.
+struct ConvPackedParams {
+  int64_t tokens, Cc, nseq, state_rows, x_row;
+  int W;
+  int io;
+  bool silu;
+  const void *x;
+  const float *w, *bias;
+  float *state;
+  const int32_t *cu, *slots;
+  void *u;
+};
+cudaError_t launch_conv1d_packed(const ConvPackedParams &p, cudaStream_t s);
+
 // The Mamba-1 scan behind ssm_scan_fwd, ssm_scan_fwd_write (t_write >= 0)
 // and ssm_scan_fwd_static (allow_cut false: the sequence is never cut into
 // segments, so the workspace is the status word and the dt-norm factors).

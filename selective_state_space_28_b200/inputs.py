@@ -279,6 +279,24 @@ def gnorm_inputs(batch, seqlen, width, io="bf16", seed=0, gate=True, weight=True
     return out
 
 
+def gdr_inputs(batch, seqlen, key_heads, heads, key_dim, value_dim, io="bf16", seed=0, h0=False,
+               device="cpu"):
+    """Inputs of one gated delta rule scan, the step's with seqlen 1: q, k and
+    v as silu leaves them, decay rates and step biases as the SSD's."""
+    g = _gen(seed, device)
+    out = {"A": -torch.exp(torch.rand(heads, generator=g, device=device) * math.log(16.0)),
+           "dt_bias": _dt_bias(heads, g, device)}
+    for name, shape in (("q", (key_heads, key_dim)), ("k", (key_heads, key_dim)),
+                        ("v", (heads, value_dim))):
+        x = _randn((batch, seqlen) + shape, g, torch.float32, device)
+        out[name] = torch.nn.functional.silu(x).to(_dtype(io))
+    for name in ("dt", "beta"):
+        out[name] = _randn((batch, seqlen, heads), g, _dtype(io), device)
+    out["h0"] = (_randn((batch, heads, key_dim, value_dim), g, torch.float32, device, 0.3)
+                 if h0 else None)
+    return out
+
+
 def workload_inputs(w: Workload, device="cpu", seed: Optional[int] = None):
     """Inputs of a scan workload (Mamba-1 or SSD)."""
     s = w.seed if seed is None else seed

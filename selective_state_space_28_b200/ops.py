@@ -12,6 +12,7 @@ returning.  This is the end-to-end path a caller with host buffers uses; for
 ssm_scan_fwd it is the library's own ssm_scan_fwd_host, which overlaps the
 copies in both directions with each other and with the scan.
 """
+import contextlib
 import ctypes
 
 import torch
@@ -21,6 +22,8 @@ from . import _lib as L
 SOFTPLUS = L.SSM_DT_SOFTPLUS
 RMS_BC = L.SSM_RMSNORM_BC
 RMS_DT = L.SSM_RMSNORM_DT
+BETA_SIGMOID = L.GDR_BETA_SIGMOID
+QK_L2NORM = L.GDR_QK_L2NORM
 
 _IO = {torch.float32: L.SSM_F32, torch.bfloat16: L.SSM_BF16}
 
@@ -401,3 +404,296 @@ def ssd_attention_fwd(dt, A, B, C, dt_bias=None, *, flags=SOFTPLUS, alpha=None,
     if sg.host:
         return sg.back((alpha,))[0]
     return alpha
+
+
+# ------------------------------------------------------------ gated delta rule
+
+_ANY_ROW = (1 << 31) - 1  # rows of a cache that is not there: only negative slots are out of range
+_GDR_FLAGS = SOFTPLUS | BETA_SIGMOID | QK_L2NORM
+
+
+@contextlib.contextmanager
+def _scope(t, stream):
+    """The device of ``t`` and ``stream`` (a torch stream or a raw handle)
+    current, so that copies, outputs and workspaces belong to the stream that
+    uses them."""
+    device = t.device if t.is_cuda else torch.device("cuda", torch.cuda.current_device())
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream) or 0, device)
+        with torch.cuda.stream(stream):
+            yield
+
+
+def _elsewhere(t, stream):
+    """Whether a call on ``t`` needs _scope."""
+    return stream is not None or (t.is_cuda and t.device.index != torch.cuda.current_device())
+
+
+def _rows(t, inner, align):
+    """``t`` [lead.., inner..] as the kernels take it: rows of dense inner
+    values at one stride.  Returns (t, stride), stride 0 for a dense tensor; a
+    tensor laid out otherwise, or off ``align`` bytes, is copied."""
+    aligned = t.data_ptr() % align == 0
+    if t.is_contiguous():
+        return (t if aligned else t.clone()), 0
+    shape, strides, lead = t.shape, t.stride(), t.dim() - inner
+    want, row = 1, 0
+    for i in range(t.dim() - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if i < lead and not row:  # the innermost axis of tokens sets the stride
+            row = strides[i]
+            aligned = aligned and row >= want
+            want = row
+        aligned = aligned and strides[i] == want
+        want *= shape[i]
+    return (t, row) if aligned else (t.contiguous(), 0)
+
+
+def _expect(name, t, dtype, shape, device):
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
+
+
+def _own(name, t):
+    """An output or cache tensor: written where it lies, so it must be dense."""
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous (it is written in place)" % name)
+    return t
+
+
+def _gdr_inputs(q, k, v, dt, A, beta, dt_bias):
+    """Checks the tensors a scan and a step share; returns their sizes."""
+    lead, (hk, K), (h, V) = tuple(v.shape[:-2]), q.shape[-2:], v.shape[-2:]
+    dev, io = v.device, v.dtype
+    _expect("q", q, io, lead + (hk, K), dev)
+    _expect("k", k, io, lead + (hk, K), dev)
+    _expect("dt", dt, io, lead + (h,), dev)
+    _expect("beta", beta, io, lead + (h,), dev)
+    if dt is not None:
+        _expect("A", A, torch.float32, (h,), dev)
+        _expect("dt_bias", dt_bias, torch.float32, (h,), dev)
+    return hk, K, h, V
+
+
+def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=None,
+                       flags=_GDR_FLAGS, l2_eps=1e-6, cu_seqlens=None, slots=None, y=None,
+                       h_last=None, workspace=None, check=False, stream=None):
+    """The gated delta rule over prompts (include/ssm.h, gdr_chunk_scan_fwd).
+
+    q, k: [b, L, Hk, K]; v: [b, L, H, V]; dt, beta: [b, L, H] (dt None: no
+    decay); A, dt_bias: [H] f32; h0: [b, H, K, V] f32; scale: K ** -0.5 unless
+    given.  Returns (y [b, L, H, V], h_last [b, H, K, V] f32).
+
+    With cu_seqlens [n + 1] int32, b is 1 and the sequences lie one behind the
+    other; h0 and h_last then have a row per sequence or, with slots [n] int32,
+    are caches of any number of rows, sequence i's state in row slots[i] (a
+    sequence whose slot is out of range is skipped; h_last must be given, and
+    may be h0).  Slices of wider tensors (dense heads, one stride between
+    tokens) are read where they lie.  With check=True (always for host
+    tensors) the stream is synchronised and an expired device wait raises."""
+    if _elsewhere(v, stream):
+        with _scope(v, stream):
+            return gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias, h0, scale=scale, flags=flags,
+                                      l2_eps=l2_eps, cu_seqlens=cu_seqlens, slots=slots, y=y,
+                                      h_last=h_last, workspace=workspace, check=check)
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("q, k and v must be [b, L, heads, dim]")
+    hk, K, h, V = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
+    b, Lq = v.shape[:2]
+    dev = v.device
+    n = b
+    if cu_seqlens is not None:
+        n = cu_seqlens.numel() - 1
+        if b != 1 or n < 0:
+            raise ValueError("cu_seqlens needs batch 1 and n + 1 entries")
+        _expect("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
+    rows = n
+    if slots is not None:
+        _expect("slots", slots, torch.int32, (n,), dev)
+        if h_last is None:
+            raise ValueError("slots needs h_last, the cache the states go to")
+        rows = h_last.shape[0]
+    _expect("h0", h0, torch.float32, (rows, h, K, V), dev)
+    _expect("h_last", h_last, torch.float32, (rows, h, K, V), dev)
+    _expect("y", y, v.dtype, (b, Lq, h, V), dev)
+    host_y, host_h = y, h_last
+    sg = None
+    if not v.is_cuda:
+        sg = _Staging([v])
+        same = h0 is not None and h_last is not None and h0.data_ptr() == h_last.data_ptr()
+        q, k, v, dt, A, beta, dt_bias, h0, cu_seqlens, slots, y = map(
+            sg.dev, (q, k, v, dt, A, beta, dt_bias, h0, cu_seqlens, slots, y))
+        h_last = h0 if same else sg.dev(h_last)
+        dev = v.device
+    q, q_row = _rows(q, 2, 16)
+    k, k_row = _rows(k, 2, 16)
+    v, v_row = _rows(v, 2, 16)
+    dt, dt_row = (None, 0) if dt is None else _rows(dt, 1, dt.element_size())
+    beta, beta_row = _rows(beta, 1, beta.element_size())
+    if h0 is not None and h0 is not h_last:
+        h0 = h0.contiguous()
+    y = torch.empty((b, Lq, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
+    h_last = (torch.empty((n, h, K, V), dtype=torch.float32, device=dev) if h_last is None
+              else _own("h_last", h_last))
+    a = L.GdrScanArgs(b, Lq, h, hk, K, V, n, rows, q_row, k_row, v_row, dt_row, beta_row,
+                      _io_of(v), flags, K ** -0.5 if scale is None else scale, l2_eps, _ptr(q),
+                      _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(_dense(A)),
+                      _ptr(_dense(dt_bias)), _ptr(h0), _ptr(_dense(cu_seqlens)),
+                      _ptr(_dense(slots)), _ptr(y), _ptr(h_last), None, 0)
+    lib = L.lib()
+    nbytes = ctypes.c_size_t(0)
+    L.check(lib.gdr_chunk_scan_workspace(ctypes.byref(a), ctypes.byref(nbytes)),
+            "gdr_chunk_scan_workspace")
+    if nbytes.value:
+        workspace = _workspace(nbytes.value, workspace, dev)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), nbytes.value
+    st = _stream(None, dev)
+    L.check(lib.gdr_chunk_scan_fwd(ctypes.byref(a), st), "gdr_chunk_scan_fwd")
+    if nbytes.value and n and (check or sg or _CHECK_ALL):
+        _check_status(workspace, st, "gdr_chunk_scan_fwd")
+    if sg is None:
+        return y, h_last
+    return _home(sg, (host_y, host_h), (y, h_last))
+
+
+def _dense(t):
+    return None if t is None else t.contiguous()
+
+
+def _home(sg, given, outs):
+    """Device outputs back in host memory: into the caller's own tensors where
+    there are some."""
+    outs = sg.back(outs)
+    return tuple(o if g is None else g.copy_(o) for g, o in zip(given, outs))
+
+
+def gdr_scan_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, flags=_GDR_FLAGS,
+                  l2_eps=1e-6, slots=None, y=None, stream=None):
+    """One decode token of the gated delta rule per sequence (include/ssm.h,
+    gdr_scan_step); ``state`` is updated in place.
+
+    q, k: [b, Hk, K]; v: [b, H, V]; dt, beta: [b, H]; state: [b, H, K, V] f32
+    or, with slots [b] int32, a cache of any number of rows (a row whose slot
+    is out of range is skipped, its y left as it was).  Returns y [b, H, V]."""
+    if _elsewhere(v, stream):
+        with _scope(v, stream):
+            return gdr_scan_step(state, q, k, v, dt, A, beta, dt_bias, scale=scale, flags=flags,
+                                 l2_eps=l2_eps, slots=slots, y=y)
+    if v.dim() != 3 or q.dim() != 3:
+        raise ValueError("q, k and v must be [b, heads, dim]")
+    hk, K, h, V = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
+    b, dev = v.shape[0], v.device
+    rows = state.shape[0] if slots is not None else b
+    _expect("slots", slots, torch.int32, (b,), dev)
+    _expect("state", _own("state", state), torch.float32, (rows, h, K, V), dev)
+    _expect("y", y, v.dtype, (b, h, V), dev)
+    host_y, host_state, sg = y, state, None
+    if not v.is_cuda:
+        sg = _Staging([v])
+        q, k, v, dt, A, beta, dt_bias, state, slots, y = map(
+            sg.dev, (q, k, v, dt, A, beta, dt_bias, state, slots, y))
+        dev = v.device
+    q, q_row = _rows(q, 2, 16)
+    k, k_row = _rows(k, 2, 16)
+    v, v_row = _rows(v, 2, 16)
+    dt, dt_row = (None, 0) if dt is None else _rows(dt, 1, dt.element_size())
+    beta, beta_row = _rows(beta, 1, beta.element_size())
+    y = torch.empty((b, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
+    a = L.GdrStepArgs(b, h, hk, K, V, rows, q_row, k_row, v_row, dt_row, beta_row, _io_of(v),
+                      flags, K ** -0.5 if scale is None else scale, l2_eps, _ptr(q), _ptr(k),
+                      _ptr(v), _ptr(dt), _ptr(beta), _ptr(_dense(A)), _ptr(_dense(dt_bias)),
+                      _ptr(_dense(slots)), _ptr(state), _ptr(y))
+    L.check(L.lib().gdr_scan_step(ctypes.byref(a), _stream(None, dev)), "gdr_scan_step")
+    if sg is None:
+        return y
+    return _home(sg, (host_y, host_state), (y, state))[0]
+
+
+def gdr_gated_rmsnorm_fwd(x, z=None, weight=None, eps=1e-5, *, out=None, stream=None):
+    """The gated delta rule's norm (include/ssm.h, gdr_gated_rmsnorm_fwd): x
+    [.., H, W] RMS-normalised over its last axis, times weight [W] f32, times
+    silu(z).  z: x's shape, or None; a slice of a wider tensor (dense heads,
+    one stride between tokens) is read where it lies.  out may be x."""
+    if _elsewhere(x, stream):
+        with _scope(x, stream):
+            return gdr_gated_rmsnorm_fwd(x, z, weight, eps, out=out)
+    if x.dim() < 2:
+        raise ValueError("x must be [.., heads, width]")
+    h, W = x.shape[-2:]
+    _expect("z", z, x.dtype, tuple(x.shape), x.device)
+    _expect("weight", weight, torch.float32, (W,), x.device)
+    _expect("out", out, x.dtype, tuple(x.shape), x.device)
+    host_out, sg = out, None
+    if not x.is_cuda:
+        sg = _Staging([x])
+        same = out is x
+        x, z, weight, out = map(sg.dev, (x, z, weight, out))
+        out = x if same else out
+    z, z_row = (None, 0) if z is None else _rows(z if z.dim() > 2 else z[None], 2, 16)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    x = _own("out", out) if x is out else x.contiguous()
+    tokens = x.numel() // (h * W) if h * W else 0
+    a = L.GdrNormArgs(tokens, h, W, z_row, _io_of(x), 0, eps, _ptr(x), _ptr(z),
+                      _ptr(_dense(weight)), _ptr(_own("out", out)))
+    L.check(L.lib().gdr_gated_rmsnorm_fwd(ctypes.byref(a), _stream(None, x.device)),
+            "gdr_gated_rmsnorm_fwd")
+    return out if sg is None else _home(sg, (host_out,), (out,))[0]
+
+
+def ssm_conv1d_packed_fwd(x, w, bias=None, state=None, *, cu_seqlens, slots=None, silu=True,
+                          u=None, stream=None):
+    """The mixers' causal depthwise convolution, then silu, over packed
+    sequences (include/ssm.h, ssm_conv1d_packed_fwd).
+
+    x: [T, C]; w: [C, W] f32 (W <= 4); bias: [C] f32; cu_seqlens: [n + 1]
+    int32; state: [n, C, W - 1] f32, updated in place, or with slots [n] int32
+    a cache of any number of rows, or None (zeros before every sequence).
+    Returns (u [T, C], state); rows of no sequence are left as they were."""
+    if _elsewhere(x, stream):
+        with _scope(x, stream):
+            return ssm_conv1d_packed_fwd(x, w, bias, state, cu_seqlens=cu_seqlens, slots=slots,
+                                         silu=silu, u=u)
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [T, C] and w [C, W]")
+    T, C = x.shape
+    W, n, dev = w.shape[1], cu_seqlens.numel() - 1, x.device
+    if n < 0:
+        raise ValueError("cu_seqlens must have n + 1 entries")
+    _expect("w", w, torch.float32, (C, W), dev)
+    _expect("bias", bias, torch.float32, (C,), dev)
+    _expect("cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
+    _expect("slots", slots, torch.int32, (n,), dev)
+    rows = n if slots is None else _ANY_ROW if state is None else state.shape[0]
+    if state is not None:
+        _expect("state", _own("state", state), torch.float32, (rows, C, W - 1), dev)
+    _expect("u", u, x.dtype, (T, C), dev)
+    host_u, host_state, sg = u, state, None
+    if not x.is_cuda:
+        sg = _Staging([x])
+        x, w, bias, state, cu_seqlens, slots, u = map(
+            sg.dev, (x, w, bias, state, cu_seqlens, slots, u))
+        dev = x.device
+    x, x_row = _rows(x, 1, 16)
+    u = torch.empty((T, C), dtype=x.dtype, device=dev) if u is None else _own("u", u)
+    a = L.ConvPackedArgs(T, C, W, n, rows, x_row, _io_of(x), L.SSM_CONV_SILU if silu else 0,
+                         _ptr(x), _ptr(_dense(w)), _ptr(_dense(bias)), _ptr(state),
+                         _ptr(_dense(cu_seqlens)), _ptr(_dense(slots)), _ptr(u))
+    L.check(L.lib().ssm_conv1d_packed_fwd(ctypes.byref(a), _stream(None, dev)),
+            "ssm_conv1d_packed_fwd")
+    if sg is None:
+        return u, state
+    if state is None:
+        return _home(sg, (host_u,), (u,))[0], None
+    return _home(sg, (host_u, host_state), (u, state))
