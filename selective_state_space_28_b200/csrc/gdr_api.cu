@@ -35,6 +35,9 @@ ssm_status_t from_cuda(cudaError_t e) {
 constexpr int64_t kMaxSize = 1ll << 31;
 constexpr double kMaxValues = 1e15;
 
+// The tensor-core scan's workspace: its status word.
+constexpr size_t kGdrStatusBytes = 256;
+
 // What the prompt scan and the step share: sizes, flags and dtype.
 template <typename Args>
 ssm_status_t check_heads(const Args *a) {
@@ -102,6 +105,18 @@ void fill_heads(ssm::GdrParams &p, const Args *a) {
   p.y = a->y;
 }
 
+ssm::GdrParams scan_params(const gdr_scan_args_t *a) {
+  ssm::GdrParams p;
+  fill_heads(p, a);
+  p.nseq = a->sequences;
+  p.L = a->seqlen;
+  p.rows = a->batch * a->seqlen;
+  p.h0 = a->h0;
+  p.h_last = a->h_last;
+  p.cu = a->cu_seqlens;
+  return p;
+}
+
 ssm_status_t check_gdr(const gdr_scan_args_t *a, bool shapes_only) {
   if (!a) return SSM_ERR_NULL;
   ssm_status_t st = check_heads(a);
@@ -136,7 +151,7 @@ ssm_status_t gdr_chunk_scan_workspace(const gdr_scan_args_t *a, size_t *bytes) {
   if (!bytes) return SSM_ERR_NULL;
   ssm_status_t st = check_gdr(a, true);
   if (st != SSM_OK) return st;
-  *bytes = 0;
+  *bytes = ssm::gdr_tc_supported(scan_params(a)) ? kGdrStatusBytes : 0;
   return SSM_OK;
 }
 
@@ -144,15 +159,13 @@ ssm_status_t gdr_chunk_scan_fwd(const gdr_scan_args_t *a, void *stream) {
   ssm_status_t st = check_gdr(a, false);
   if (st != SSM_OK) return st;
   if (a->sequences == 0) return SSM_OK;  // nothing to do, nothing launched
-  ssm::GdrParams p;
-  fill_heads(p, a);
-  p.nseq = a->sequences;
-  p.L = a->seqlen;
-  p.rows = a->batch * a->seqlen;
-  p.h0 = a->h0;
-  p.h_last = a->h_last;
-  p.cu = a->cu_seqlens;
-  return from_cuda(ssm::launch_gdr_recurrent(p, static_cast<cudaStream_t>(stream)));
+  const ssm::GdrParams p = scan_params(a);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (!ssm::gdr_tc_supported(p)) return from_cuda(ssm::launch_gdr_recurrent(p, cs));
+  if (!a->workspace || a->workspace_bytes < kGdrStatusBytes) return SSM_ERR_WORKSPACE;
+  int *status = static_cast<int *>(a->workspace);
+  if (cudaMemsetAsync(status, 0, sizeof(int), cs) != cudaSuccess) return SSM_ERR_CUDA;
+  return from_cuda(ssm::launch_gdr_tc(p, status, cs));
 }
 
 ssm_status_t gdr_scan_step(const gdr_step_args_t *a, void *stream) {
