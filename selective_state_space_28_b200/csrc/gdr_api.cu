@@ -35,9 +35,6 @@ ssm_status_t from_cuda(cudaError_t e) {
 constexpr int64_t kMaxSize = 1ll << 31;
 constexpr double kMaxValues = 1e15;
 
-// The tensor-core scan's workspace: its status word.
-constexpr size_t kGdrStatusBytes = 256;
-
 // What the prompt scan and the step share: sizes, flags and dtype.
 template <typename Args>
 ssm_status_t check_heads(const Args *a) {
@@ -151,7 +148,8 @@ ssm_status_t gdr_chunk_scan_workspace(const gdr_scan_args_t *a, size_t *bytes) {
   if (!bytes) return SSM_ERR_NULL;
   ssm_status_t st = check_gdr(a, true);
   if (st != SSM_OK) return st;
-  *bytes = ssm::gdr_tc_supported(scan_params(a)) ? kGdrStatusBytes : 0;
+  const ssm::GdrParams p = scan_params(a);
+  *bytes = ssm::gdr_tc_supported(p) ? ssm::gdr_tc_workspace(p) : 0;
   return SSM_OK;
 }
 
@@ -162,10 +160,8 @@ ssm_status_t gdr_chunk_scan_fwd(const gdr_scan_args_t *a, void *stream) {
   const ssm::GdrParams p = scan_params(a);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!ssm::gdr_tc_supported(p)) return from_cuda(ssm::launch_gdr_recurrent(p, cs));
-  if (!a->workspace || a->workspace_bytes < kGdrStatusBytes) return SSM_ERR_WORKSPACE;
-  int *status = static_cast<int *>(a->workspace);
-  if (cudaMemsetAsync(status, 0, sizeof(int), cs) != cudaSuccess) return SSM_ERR_CUDA;
-  return from_cuda(ssm::launch_gdr_tc(p, status, cs));
+  if (!a->workspace || a->workspace_bytes < ssm::gdr_tc_workspace(p)) return SSM_ERR_WORKSPACE;
+  return from_cuda(ssm::launch_gdr_tc(p, a->workspace, cs));
 }
 
 ssm_status_t gdr_scan_step(const gdr_step_args_t *a, void *stream) {

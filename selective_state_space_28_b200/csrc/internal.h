@@ -175,9 +175,11 @@ struct GdrParams {
 constexpr int64_t kGdrMaxKeyDim = 256;
 cudaError_t launch_gdr_recurrent(const GdrParams &p, cudaStream_t s);
 // The chunked scan on the tensor cores: the shapes it takes (pointers not
-// looked at), and its launch (`status`: the call's status word).
+// looked at, `cu` aside), its workspace (the status word first), its launches.
+constexpr size_t kGdrStatusBytes = 256;
 bool gdr_tc_supported(const GdrParams &p);
-cudaError_t launch_gdr_tc(const GdrParams &p, int *status, cudaStream_t s);
+size_t gdr_tc_workspace(const GdrParams &p);
+cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s);
 cudaError_t launch_gdr_step(const GdrParams &p, cudaStream_t s);
 
 // RMS norm per head, then the gate.
