@@ -134,13 +134,32 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
-// x = hi + lo in float16 pairs.
+// x = hi + lo in float16 pairs (x - hi by a multiply-add that takes float16
+// factors: at full rate, where a conversion back and a packed sum take three
+// times as long).
 __device__ __forceinline__ void split_h2(f2 x, uint32_t &hi, uint32_t &lo) {
-  const __half2 h = __floats2half2_rn(x.x, x.y);
-  const float2 b = __half22float2(h);
-  const f2 r = add2(x, mk2(-b.x, -b.y));
-  hi = *reinterpret_cast<const uint32_t *>(&h);
-  lo = pack_h2(r.x, r.y);
+  hi = pack_h2(x.x, x.y);
+  float a, b;
+  asm("{\n\t.reg .f16 h0, h1, m;\n\tmov.b32 {h0, h1}, %2;\n\tmov.b16 m, 0xbc00;\n\t"
+      "fma.rn.f32.f16 %0, h0, m, %3;\n\tfma.rn.f32.f16 %1, h1, m, %4;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "r"(hi), "f"(x.x), "f"(x.y));
+  lo = pack_h2(a, b);
+}
+// max(|a|, |b|) of float16 pairs (the sign bits are not part of the result).
+__device__ __forceinline__ uint32_t maxabs_h2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two bfloat16 times a bfloat16, plus c, in float32.
+__device__ __forceinline__ f2 fma_bf16x2(uint32_t x, uint32_t y, f2 c) {
+  f2 d;
+  asm("{\n\t.reg .b16 x0, x1, y0, y1;\n\tmov.b32 {x0, x1}, %2;\n\tmov.b32 {y0, y1}, %3;\n\t"
+      "fma.rn.f32.bf16 %0, x0, y0, %4;\n\tfma.rn.f32.bf16 %1, x1, y1, %5;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(x), "r"(y), "f"(c.x), "f"(c.y));
+  return d;
 }
 
 // 2^e, e clamped to the normal range.
@@ -177,17 +196,67 @@ template <int KD> struct __align__(1024) PrepSmem {
     };
   };
   f2 g[kC];  // running sum of log2 of the decays, hi and lo
-  float beta[kC], f[kC], f31[kC / 2], qq[kC];
+  float beta[kC], f[kC], h[kC], qq[kC];
   float bkn[2], tn[4];
   uint64_t full, done;
   uint32_t taddr;
 };
 
+// C (+)= A B in float32 on the tensor cores' tf32: both operands as hi + lo,
+// three products.  C [16 x 8], A [16 x 8] rows and B [8 x 8] in mma.m16n8k8's
+// lane layout.
+__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // 11 bits, to nearest
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// out [16 MT x 8] = a [16 MT x 8 KT] b [8 KT x 8], rows of kAm floats.
+template <int MT, int KT>
+__device__ __forceinline__ void small_product(const float *a, const float *b, float (&out)[MT][4]) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[m][e] = 0.f;
+#pragma unroll
+  for (int k = 0; k < KT; ++k) {
+    uint32_t bh[2], bl[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) split_tf32(b[(8 * k + t + 4 * e) * kAm + r], bh[e], bl[e]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      uint32_t ah[4], al[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        split_tf32(a[(16 * m + r + 8 * (e & 1)) * kAm + 8 * k + t + 4 * (e >> 1)], ah[e], al[e]);
+      mma_tf32(out[m], al, bh);
+      mma_tf32(out[m], ah, bl);
+      mma_tf32(out[m], ah, bh);
+    }
+  }
+}
+template <int MT>
+__device__ __forceinline__ void put_product(float *o, const float (&c)[MT][4], float sign) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      *reinterpret_cast<float2 *>(&o[(16 * m + r + 8 * e) * kAm + 2 * t]) =
+          make_float2(sign * c[m][2 * e], sign * c[m][2 * e + 1]);
+}
+
 // One CTA of 128 threads per (chunk, value head).  Row pt of [K; Q] [K]^T is
 // thread pt's (TMEM lane pt): keys' rows make A, queries' P.  The inverse goes
-// by blocks: the two 32 x 32 diagonal blocks by forward substitution, a column
-// a lane, then -T22 A21 T11 below them, in float32.  Bound by issue slots
-// (about 1100 warp instructions a scheduler), several CTAs to an SM.
+// by blocks: the four 16 x 16 diagonal blocks by forward substitution, a column
+// a lane; then twice -T22 A21 T11 for the block below two of them, the products
+// as float32 on mma (a multiply-add version read its operands from shared memory
+// four times as often, which bound the kernel: 4200 cycles a unit of SM time).
 template <int KD>
 __global__ void __launch_bounds__(kPrepThreads)
     gdr_prep_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mQ,
@@ -300,10 +369,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[ch >> 3][0] + sw128(kC + row, ch & 7));
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f2 x = mk2(bf16lo(w[e]), bf16hi(w[e]));
-        a = fma2(x, x, a);
-      }
+      for (int e = 0; e < 4; ++e) a = fma_bf16x2(w[e], w[e], a);
     }
     float n2 = a.x + a.y;
     n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
@@ -342,7 +408,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (p.flags & GDR_QK_L2NORM) nf = n2 == 0.f ? 0.f : nf / sqrtf(n2 + p.l2_eps);
     if (n2 != n2) nf = n2;
   }
-  const f2 gi = s.g[tok], g31 = s.g[31], g63 = s.g[63];
+  const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
   const float eg = ex2(gi.x + gi.y);
   float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, bv) - kRecT));
   float rowf = f;
@@ -354,7 +420,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     fac[2 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));       // cu
     fac[5 * kC + tok] = f;                                          // fk
     s.f[tok] = f;
-    if (tok < 32) s.f31[tok] = f * ex2((g31.x - gi.x) + (g31.y - gi.y));
+    s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
     const float m = warp_max(2.f * fabsf(nb * eg));
     if (lane == 0) s.bkn[pw] = m;
   } else {
@@ -363,39 +429,52 @@ __global__ void __launch_bounds__(kPrepThreads)
     fac[4 * kC + tok] = cq;       // cqp
     fac[6 * kC + tok] = f;        // fq
   }
-  __syncthreads();  // f, f31
+  __syncthreads();  // f, h
 
-  // A and P: this row's columns of its own 32-token block, and of the first
-  // block for a row of the second
+  // A and P, 16 columns at a time.  In the row's own 16-token block the decays
+  // are taken element by element; in blocks before it they go by way of the
+  // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
+  // above 1.
   uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
-  const int blk = pw & 1;
+  const int blk = pw & 1, own = tok >> 4;
+  float dec[16];
 #pragma unroll
-  for (int J = 0; J < 4; ++J) {  // 16 columns
-    if ((J >> 1) > blk) break;
-    uint32_t r[16];
+  for (int q = 0; q < 16; ++q) {
+    const int j = 16 * own + q;
+    const f2 gj = s.g[j];
+    const f2 d = add2(gi, mk2(-gj.x, -gj.y));
+    const bool in = on && (isk ? j < tok : j <= tok);
+    dec[q] = in ? rowf * s.f[j] * ex2(d.x + d.y) : 0.f;
+  }
+#pragma unroll
+  for (int J = 0; J < 4; ++J) {
     float x[16];
-    tmem_ld16(grow + 16 * J, r);
-    tmem_ld_wait();
-    if ((J >> 1) == blk) {
+    if ((J >> 1) <= blk) {
+      uint32_t r[16];
+      tmem_ld16(grow + 16 * J, r);
+      const f2 ge = s.g[16 * J + 15];
+      const float fr = on && J < own ? rowf * ex2((gi.x - ge.x) + (gi.y - ge.y)) : 0.f;
+      float w[16];
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
-        const int j = 16 * J + q;
-        const f2 gj = s.g[j];
-        const f2 d = add2(gi, mk2(-gj.x, -gj.y));
-        const bool in = on && (isk ? j < tok : j <= tok);
-        x[q] = in ? __uint_as_float(r[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
+        w[q] = fr * s.h[16 * J + q];
+        if (J == own) w[q] = dec[q];
       }
-    } else {
-      const float fr = rowf * ex2((gi.x - g31.x) + (gi.y - g31.y));
+      tmem_ld_wait();
+      // (a product that is left out may be anything, NaN included)
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        x[q] = on ? __uint_as_float(r[q]) * (fr * s.f31[16 * J + q]) : 0.f;
+      for (int q = 0; q < 16; ++q) x[q] = w[q] != 0.f ? __uint_as_float(r[q]) * w[q] : 0.f;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) x[q] = 0.f;
     }
     if (isk) {
+      if ((J >> 1) <= blk) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
-            make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
+              make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -406,17 +485,17 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
   tc_fence_before();
   if (isk) {
-    // the inverse of this warp's diagonal block, a column a lane
+    // the inverses of this warp's two diagonal blocks, a column a lane
     __syncwarp();
-    const int o = 32 * pw;
-    f2 x[16];
+    const int o = 32 * pw + (lane & 16), col = lane & 15;
+    f2 x[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      f2 a0 = mk2(lane == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
+    for (int i = 0; i < 16; ++i) {
+      f2 a0 = mk2(col == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
 #pragma unroll
       for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
         const float4 a = *reinterpret_cast<const float4 *>(&s.Am[o + i][o + 4 * j4]);
-        // (columns from i on hold zeros, or x not yet set is not read)
+        // (columns from i on hold zeros; x not yet set is not read)
         if (4 * j4 + 1 < i) a0 = fma2(mk2(-a.x, -a.y), x[2 * j4], a0);
         else a0.x = fmaf(-a.x, x[2 * j4].x, a0.x);
         if (4 * j4 + 3 < i) a1 = fma2(mk2(-a.z, -a.w), x[2 * j4 + 1], a1);
@@ -426,57 +505,38 @@ __global__ void __launch_bounds__(kPrepThreads)
       const float xi = a0.x + a0.y;
       if (i & 1) x[i / 2].y = xi; else x[i / 2].x = xi;
     }
-    __syncwarp();  // every lane has read the block
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s.Am[o + 2 * i][o + lane] = x[i].x;
-      s.Am[o + 2 * i + 1][o + lane] = x[i].y;
-    }
-  }
-  __syncthreads();
-  {  // X = A21 T11, rows 8 pw .. + 8, a column a lane
-    f2 acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = mk2(0.f, 0.f);
-#pragma unroll
-    for (int j4 = 0; j4 < 8; ++j4) {
-      const f2 t01 = mk2(s.Am[4 * j4][lane], s.Am[4 * j4 + 1][lane]);
-      const f2 t23 = mk2(s.Am[4 * j4 + 2][lane], s.Am[4 * j4 + 3][lane]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 a = *reinterpret_cast<const float4 *>(&s.Am[32 + 8 * pw + i][4 * j4]);
-        acc[i] = fma2(mk2(a.x, a.y), t01, acc[i]);
-        acc[i] = fma2(mk2(a.z, a.w), t23, acc[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s.Am[8 * pw + i][32 + lane] = acc[i].x + acc[i].y;
-  }
-  __syncthreads();
-  {  // T21 = -T22 X
-    f2 acc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = mk2(0.f, 0.f);
-#pragma unroll
-    for (int j4 = 0; j4 < 8; ++j4) {
-      const f2 t01 = mk2(s.Am[4 * j4][32 + lane], s.Am[4 * j4 + 1][32 + lane]);
-      const f2 t23 = mk2(s.Am[4 * j4 + 2][32 + lane], s.Am[4 * j4 + 3][32 + lane]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 a = *reinterpret_cast<const float4 *>(&s.Am[32 + 8 * pw + i][32 + 4 * j4]);
-        acc[i] = fma2(mk2(a.x, a.y), t01, acc[i]);
-        acc[i] = fma2(mk2(a.z, a.w), t23, acc[i]);
-      }
-    }
+    __syncwarp();  // every lane has read the blocks
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float t = -(acc[i].x + acc[i].y);
-      s.Am[32 + 8 * pw + i][lane] = t;
+      s.Am[o + 2 * i][o + col] = x[i].x;
+      s.Am[o + 2 * i + 1][o + col] = x[i].y;
     }
   }
   __syncthreads();
-  // T to float16 pairs: row pt / 2, half pt % 2 (the block above the diagonal
-  // ones is never read)
+  {  // below the diagonal blocks of 16: half pw & 1 of the columns of pair pw / 2
+    const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
+    float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
+    float c1[1][4], c2[1][4];
+    small_product<1, 2>(&s.Am[o + 16][o], &s.Am[o][o + n], c1);
+    put_product<1>(scratch, c1, 1.f);
+    __syncwarp();
+    small_product<1, 2>(&s.Am[o + 16][o + 16], scratch, c2);
+    __syncthreads();  // A21 has been read
+    put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
+  }
+  __syncthreads();
+  {  // and of 32: eight columns a warp
+    float *scratch = &s.Am[0][32 + 8 * pw];
+    float c1[2][4], c2[2][4];
+    small_product<2, 4>(&s.Am[32][0], &s.Am[0][8 * pw], c1);
+    put_product<2>(scratch, c1, 1.f);
+    __syncwarp();
+    small_product<2, 4>(&s.Am[32][32], scratch, c2);
+    __syncthreads();
+    put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
+  }
+  __syncthreads();
+  // T to float16 pairs: row pt / 2, half pt % 2
   const int row = pt >> 1, hf = pt & 1;
   const bool have = hf <= (row >> 5);
   f2 t[16];
@@ -524,7 +584,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     bulk_store(out, s.T, kRecT);
     bulk_store(out + kRecT, s.rest, sizeof(Rec) - kRecT);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   }
 }
 
@@ -552,10 +612,11 @@ template <int KD> struct __align__(1024) GdrSmem {
   uint8_t kq[3][KD / 64][128 * 128];  // [stage][slab]: rows 0-63 keys, 64-127 queries
   __nv_bfloat16 v[2][kC][kV];
   struct __align__(1024) { Rec r; } rec[2];
-  // maxima, by lane quarter and half; of a chunk's y, the scales of QS and PU
-  float vmax[4][2], smax[4][2], rmax[4][2], umax[4][2], ysc[2][4][2];
-  uint64_t fullk[3], conv[3], empty[3], fullr[2], ofree[2], supdone[2], sready[2];
-  uint64_t ksdone, rready, udone, uready, pudone;
+  // maxima, by lane quarter and half; of a chunk's y, the scales of QS and PU,
+  // and a warp's factors with them
+  float vmax[4][2], smax[4][2], ysc[2][4][2], yfac[4][2][kC];
+  uint64_t fullk[3], conv[3], empty[3], fullr[2], ofree[2], sready[2];
+  uint64_t ksdone, rready, udone, uready, supdone, pudone;
   uint32_t taddr;
 };
 static_assert(sizeof(GdrSmem<128>) + 1024 <= 232448, "GdrSmem exceeds the shared memory of a CTA");
@@ -620,13 +681,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.fullr[i], 1);
       mbar_init(&s.ofree[i], 4);
-      mbar_init(&s.supdone[i], 1);
       mbar_init(&s.sready[i], 4);
     }
     mbar_init(&s.ksdone, 1);
     mbar_init(&s.rready, 8);
     mbar_init(&s.udone, 1);
     mbar_init(&s.uready, 8);
+    mbar_init(&s.supdone, 1);
     mbar_init(&s.pudone, 1);
     fence_mbar_init();
   }
@@ -679,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- MMA issuer
       const bool leader = elect_one();
       const uint32_t id64 = idesc_f16_f32(128, 64, false);
-      const uint32_t idS = idesc_f16_f32(128, 64, true);
+      const uint32_t idS = idesc_f16_f32(128, KD, true);
       uint64_t *last_bar = nullptr;
       uint32_t last_par = 0;
       auto commit = [&](uint64_t *bar, uint32_t par) {
@@ -694,12 +755,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scol = [](int kk) { return kColS + (kk / (KH / 16)) * KH + (kk % (KH / 16)) * 8; };
       // of K step kk of R, U and U' (lo: 16 further on)
       auto rcol = [](int kk) { return 32 * (kk >> 1) + 8 * (kk & 1); };
-      // K step kk of a product with T or P, which hold zeros above their
-      // diagonals: outputs of tokens before 16 kk are left out
-      auto tri = [&](uint32_t d, uint32_t a, uint64_t b, int kk, bool more) {
-        mma_ts(d + 16 * kk, a + rcol(kk), b + (uint64_t)(kk * (2048 + 32) >> 4),
-               idesc_f16_f32(128, 64 - 16 * kk, false), more);
-      };
       for (int c = 0; c < nch; ++c) {
         const uint32_t ph = c & 1, php = (c - 1) & 1;
         const uint64_t dk = smem_desc(smem_u32(s.kq[c % 3][0]), 16, 1024, kSwizzle128B);
@@ -744,7 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 3; ++x)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tri(tb + kColKS, tb + kColR + (x == 1 ? 16 : 0), x == 2 ? tl : th, kk, x + kk > 0);
+              mma_ts(tb + kColKS, tb + kColR + rcol(kk) + (x == 1 ? 16 : 0),
+                     (x == 2 ? tl : th) + 2 * kk, id64, x + kk > 0);
         }
         commit(&s.udone, ph);
         wait(&s.uready, ph, 8);
@@ -752,19 +808,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (leader) {
 #pragma unroll
-          for (int h = 0; h < NP; ++h) {  // 64 key dimensions: a slab
+          for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ts(tb + kColS + 64 * h, tb + kColU2 + rcol(kk) + 16 * x,
-                       dm + (uint64_t)((h * 128 * 128 + kk * 2048) >> 4), idS, x + kk > 0);
-            mma_commit(&s.supdone[h]);
-          }
-          if (NP == 1) mma_commit(&s.supdone[1]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(tb + kColS, tb + kColU2 + rcol(kk) + 16 * x, dm + kk * 128, idS, x + kk > 0);
+          mma_commit(&s.supdone);
           mma_commit(&s.empty[c % 3]);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tri(tb + kColPU, tb + kColR, dp, kk, kk > 0);
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(tb + kColPU, tb + kColR + rcol(kk), dp + 2 * kk, id64, kk > 0);
         }
         commit(&s.pudone, ph);
       }
@@ -785,8 +837,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&s.fullr[par], (c >> 1) & 1, 9);
       wait(&s.pudone, par, 10);
       tc_fence_after();
-      const f2 fQ = mk2(s.ysc[par][quarter][0], s.ysc[par][quarter][0]);
-      const f2 fP = mk2(s.ysc[par][quarter][1], s.ysc[par][quarter][1]);
+      // this warp's factors of the tokens
+      const float fQ = s.ysc[par][quarter][0], fP = s.ysc[par][quarter][1];
+      float(*yf)[kC] = s.yfac[quarter];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        yf[0][lane + 32 * e] = rc.cqe[lane + 32 * e] * fQ;
+        yf[1][lane + 32 * e] = rc.cqp[lane + 32 * e] * fP;
+      }
+      __syncwarp();
       __nv_bfloat16 *yp = yb + (int64_t)c * kC * yrow;
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
@@ -796,24 +855,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 ce = *reinterpret_cast<const float4 *>(&rc.cqe[16 * i + 4 * q]);
-          const float4 cp = *reinterpret_cast<const float4 *>(&rc.cqp[16 * i + 4 * q]);
+          const float4 ce = *reinterpret_cast<const float4 *>(&yf[0][16 * i + 4 * q]);
+          const float4 cp = *reinterpret_cast<const float4 *>(&yf[1][16 * i + 4 * q]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int k = 4 * q + 2 * e;
-            const f2 qs = mul2(mk2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), fQ);
-            const f2 pu = mul2(mk2(__uint_as_float(u[k]), __uint_as_float(u[k + 1])), fP);
+            const f2 qs = mk2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+            const f2 pu = mk2(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
             const f2 o = fma2(e ? mk2(ce.z, ce.w) : mk2(ce.x, ce.y), qs,
                               mul2(e ? mk2(cp.z, cp.w) : mk2(cp.x, cp.y), pu));
             out[2 * q + e] = pack_bf16x2(o.x, o.y);
           }
         }
-        if (live) {
+        if (live && 16 * i + 16 <= nv) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (16 * i + j < nv)
-              *reinterpret_cast<uint16_t *>(yp + (16 * i + j) * yrow) =
-                  (uint16_t)(out[j / 2] >> (16 * (j & 1)));
+          for (int j = 0; j < 16; ++j) {
+            *reinterpret_cast<uint16_t *>(yp) = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
+            yp += yrow;
+          }
+        } else if (live) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            if (16 * i + j < nv) *reinterpret_cast<uint16_t *>(yp) = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
+            yp += yrow;
+          }
         }
       }
       tc_fence_before();
@@ -829,6 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t left = len - (int64_t)c * kC;
       wait(&s.fullr[par], (c >> 1) & 1, 11);
       const float f = pt < 64 ? s.rec[par].r.fk[tok] : s.rec[par].r.fq[tok];
+      const uint32_t f2x = __byte_perm(__float_as_uint(f), 0, 0x3232);  // (a power of two: exact)
       wait(&s.fullk[c % 3], (c / 3) & 1, 12);
       uint8_t *base = &s.kq[c % 3][0][0];
       const bool on = tok < left;  // rows behind the end may hold anything
@@ -839,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const f2 y = mul2(mk2(bf16lo(w[x]), bf16hi(w[x])), mk2(f, f));
+          const f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
           w[x] = on ? pack_h2(y.x, y.y) : 0u;
         }
         *at = make_uint4(w[0], w[1], w[2], w[3]);
@@ -852,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ the chain
     reg_alloc<kRegChain>();
     const float kNorm = KD == 128 ? 11.32f : 8.f;  // sqrt(KD): |S^T k| <= |k| sqrt(KD) max |S|
-    f2 st[KH / 2];  // the half row of this lane
+    f2 st[KH / 2];  // the half row of this lane, scaled by 2^eS
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < KH; ++i) {
@@ -864,7 +930,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     m = warp_max(m);
     if (lane == 0) s.smax[quarter][ch] = m;
     pair_sync(quarter);
-    int eS = scale_exp(fmaxf(s.smax[quarter][0], s.smax[quarter][1]));
+    float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
+    int eS = scale_exp(smax);
     // S's pieces, hi and lo of each half within the half's own dS columns
     const uint32_t mycol = tb + lane_base + kColS + ch * KH;
     {
@@ -873,7 +940,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < KH / 32; ++i) {
         uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) split_h2(mul2(st[16 * i + j], sc), hi[j], lo[j]);
+        for (int j = 0; j < 16; ++j) {
+          st[16 * i + j] = mul2(st[16 * i + j], sc);
+          split_h2(st[16 * i + j], hi[j], lo[j]);
+        }
         tmem_st16(mycol + 16 * i, hi);
         tmem_st16(mycol + KH / 2 + 16 * i, lo);
       }
@@ -883,16 +953,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sready[ch]);
 
-    for (int c = 0; c < nch; ++c) {
+    // b v of chunk c, and its maximum
+    f2 x[16];
+    auto values = [&](int c) {
       const int par = c & 1;
-      const uint32_t ph = par;
       const int64_t left = len - (int64_t)c * kC;
       const int nv = (int)(left < kC ? left : kC);
       const Rec &rc = s.rec[par].r;
-      // before KS is there: b v, and R's scale
       wait(&s.fullr[par], (c >> 1) & 1, 13);
-      f2 x[16], nb[16];
-      m = 0.f;
+      float m = 0.f;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         const int j = 32 * ch + 4 * q;
@@ -910,16 +979,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = fmaxf(fmaxf(m, fabsf(x[2 * q].x)), fabsf(x[2 * q].y));
         m = fmaxf(fmaxf(m, fabsf(x[2 * q + 1].x)), fabsf(x[2 * q + 1].y));
       }
-      const float gC = rc.gC, tn = rc.tn;
-      const int eT = (int)rc.eT;
       m = warp_max(m);
       if (lane == 0) s.vmax[quarter][ch] = m;
+    };
+    values(0);
+    for (int c = 0; c < nch; ++c) {
+      const int par = c & 1;
+      const uint32_t ph = par;
+      const Rec &rc = s.rec[par].r;
+      // While KS runs: the chunk's scales.  |R| <= bR, |U| <= |T| bR row by
+      // row, |dS| <= sum |k| |U| <= 128 max |U|: R and U take one scale, U' the
+      // next state's, so that dS comes out in it.
       pair_sync(quarter);
-      const float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
-      const int eR = scale_exp(fmaxf(s.vmax[quarter][0], s.vmax[quarter][1]) + rc.bkn * kNorm * smax);
+      if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
+      const float gC = rc.gC;
+      const int eT = (int)rc.eT;
+      const float tn = rc.tn * pow2i(-eT);
+      const float bR = fmaxf(s.vmax[quarter][0], s.vmax[quarter][1]) + rc.bkn * kNorm * smax;
+      const int eR = scale_exp(bR * fmaxf(tn, 1.f));
+      const int eN = scale_exp(fabsf(gC) * smax + 128.f * (tn * bR));
+      f2 nb[16];
       {
-        const f2 fR = mk2(pow2i(eR), pow2i(eR));
-        const f2 fK = mk2(-pow2i(-eS), -pow2i(-eS));
+        const f2 fR = mk2(pow2i(eR), pow2i(eR)), fK = mk2(-pow2i(-eS), -pow2i(-eS));
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float4 bk = *reinterpret_cast<const float4 *>(&rc.bk[32 * ch + 4 * q]);
@@ -929,6 +1010,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           nb[2 * q + 1] = mul2(mul2(mk2(bk.z, bk.w), fK), fR);
         }
       }
+      if (ch == 0 && lane == 0) {
+        s.ysc[par][quarter][0] = pow2i(-eS);
+        s.ysc[par][quarter][1] = pow2i(-eR - eT);
+      }
       // R
       wait(&s.ksdone, ph, 14);
       tc_fence_after();
@@ -937,13 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(tb + lane_base + kColKS + 32 * ch, r0);
         tmem_ld16(tb + lane_base + kColKS + 32 * ch + 16, r1);
         tmem_ld_wait();
-        m = 0.f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const uint32_t a = q < 8 ? r0[2 * q] : r1[2 * q - 16], b = q < 8 ? r0[2 * q + 1] : r1[2 * q - 15];
-          x[q] = fma2(nb[q], mk2(__uint_as_float(a), __uint_as_float(b)), x[q]);
-          m = fmaxf(fmaxf(m, fabsf(x[q].x)), fabsf(x[q].y));
-          split_h2(x[q], hi[q], lo[q]);
+          split_h2(fma2(nb[q], mk2(__uint_as_float(a), __uint_as_float(b)), x[q]), hi[q], lo[q]);
         }
         tmem_st16(tb + lane_base + kColR + 32 * ch, hi);
         tmem_st16(tb + lane_base + kColR + 32 * ch + 16, lo);
@@ -953,21 +1035,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.rready);
       // U and U'
-      m = warp_max(m);
-      if (lane == 0) s.rmax[quarter][ch] = m;  // of R 2^eR
-      pair_sync(quarter);
-      int eU = scale_exp(tn * fmaxf(s.rmax[quarter][0], s.rmax[quarter][1]));  // of U 2^(eR + eT)
-      const f2 fU = mk2(pow2i(eU), pow2i(eU));
-      eU += eR + eT;
-      if (ch == 0 && lane == 0) {
-        s.ysc[par][quarter][0] = pow2i(-eS);
-        s.ysc[par][quarter][1] = pow2i(-eU);
-      }
+      {
+        const f2 fU = mk2(pow2i(eN - eR - eT), pow2i(eN - eR - eT));
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 cu = *reinterpret_cast<const float4 *>(&rc.cu[32 * ch + 4 * q]);
-        nb[2 * q] = mk2(cu.x, cu.y);
-        nb[2 * q + 1] = mk2(cu.z, cu.w);
+        for (int q = 0; q < 8; ++q) {
+          const float4 cu = *reinterpret_cast<const float4 *>(&rc.cu[32 * ch + 4 * q]);
+          nb[2 * q] = mul2(mk2(cu.x, cu.y), fU);
+          nb[2 * q + 1] = mul2(mk2(cu.z, cu.w), fU);
+        }
       }
       wait(&s.udone, ph, 15);
       tc_fence_after();
@@ -976,15 +1051,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16(tb + lane_base + kColKS + 32 * ch, r0);
         tmem_ld16(tb + lane_base + kColKS + 32 * ch + 16, r1);
         tmem_ld_wait();
-        m = 0.f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const uint32_t a = q < 8 ? r0[2 * q] : r1[2 * q - 16], b = q < 8 ? r0[2 * q + 1] : r1[2 * q - 15];
-          f2 y = mul2(mk2(__uint_as_float(a), __uint_as_float(b)), fU);
+          const f2 y = mk2(__uint_as_float(a), __uint_as_float(b));
           uh[q] = pack_h2(y.x, y.y);
-          y = mul2(y, nb[q]);
-          m = fmaxf(fmaxf(m, fabsf(y.x)), fabsf(y.y));
-          split_h2(y, hi[q], lo[q]);
+          split_h2(mul2(y, nb[q]), hi[q], lo[q]);
         }
         tmem_st16(tb + lane_base + kColU2 + 32 * ch, hi);
         tmem_st16(tb + lane_base + kColU2 + 32 * ch + 16, lo);
@@ -994,19 +1066,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.uready);
-      m = warp_max(m);
-      if (lane == 0) s.umax[quarter][ch] = m;  // of U' 2^eU
-      pair_sync(quarter);
-      // the state: |dS| <= sum |k| |U'| <= 128 max |U'|
-      const float fD = pow2i(-eU);
-      eS = scale_exp(fabsf(gC) * smax + 128.f * (fmaxf(s.umax[quarter][0], s.umax[quarter][1]) * fD));
-      wait(&s.supdone[ch], ph, 16);
+      // while dS runs: the next chunk's values
+      if (c + 1 < nch) values(c + 1);
+      // the state
+      wait(&s.supdone, ph, 16);
       tc_fence_after();
       {
-        const f2 g2 = mk2(gC, gC), fD2 = mk2(fD, fD), fS2 = mk2(pow2i(eS), pow2i(eS));
-        uint32_t r[2][16];
-        m = 0.f;
-        uint32_t hi[KH / 2], lo[KH / 2];
+        const float gn = gC * pow2i(eN - eS);  // (the difference beyond the range: all or nothing is left)
+        const f2 g2 = mk2(gn, gn);
+        eS = eN;
+        uint32_t r[2][16], hi[KH / 2], lo[KH / 2], mh = 0u;
 #pragma unroll
         for (int i = 0; i < KH / 32; ++i) {
           tmem_ld16(mycol + 32 * i, r[0]);
@@ -1016,9 +1085,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j) {
             f2 &v = st[16 * i + j];
             const uint32_t a = r[j >> 3][2 * (j & 7)], b = r[j >> 3][2 * (j & 7) + 1];
-            v = fma2(v, g2, mul2(mk2(__uint_as_float(a), __uint_as_float(b)), fD2));
-            m = fmaxf(fmaxf(m, fabsf(v.x)), fabsf(v.y));
-            split_h2(mul2(v, fS2), hi[16 * i + j], lo[16 * i + j]);
+            v = fma2(v, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
+            split_h2(v, hi[16 * i + j], lo[16 * i + j]);
+            mh = maxabs_h2(mh, hi[16 * i + j]);
           }
         }
         // (this warp's own dS columns, all read)
@@ -1027,6 +1096,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st16(mycol + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(&hi[16 * i]));
           tmem_st16(mycol + KH / 2 + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(&lo[16 * i]));
         }
+        const uint32_t a = mh & 0x7fffu, b = (mh >> 16) & 0x7fffu;  // float16 order is that of the bits
+        mh = a > b ? a : b;
+        // (hi may lie half a step, 2^-11, below the value)
+        m = mh < 0x7c00u ? 1.001f * __half2float(__ushort_as_half((unsigned short)mh)) : 0.f;
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1036,10 +1109,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) s.smax[quarter][ch] = m;
     }
     if (p.h_last && live && !wait.dead) {
+      const float un = pow2i(-eS);
 #pragma unroll
       for (int i = 0; i < KH; ++i) {
         const int r = ch * KH + i;
-        if (r < p.K) p.h_last[so + (int64_t)r * p.V + cv] = (i & 1) ? st[i / 2].y : st[i / 2].x;
+        if (r < p.K) p.h_last[so + (int64_t)r * p.V + cv] = un * ((i & 1) ? st[i / 2].y : st[i / 2].x);
       }
     }
   }
