@@ -68,8 +68,9 @@ struct Rec {
   uint8_t P[kC * 128];
   float bv[kC], bk[kC], cu[kC], cqe[kC], cqp[kC];  // factors of V, KS, U', QS, PU
   float fk[kC], fq[kC];                            // powers of two of keys and queries
-  float gC, bkn, tn, eT;  // e^g_63; bound of bk |k|; of T's rows (scaled); T's exponent
-  float pad[12];
+  // e^g_63; bounds of bk |k|, of T's rows (scaled), of bv; T's exponent
+  float gC, bkn, tn, bvn, eT;
+  float pad[11];
 };
 constexpr size_t kRecT = 2 * kC * 128;
 static_assert(sizeof(Rec) == 26432 && sizeof(Rec) % 16 == 0, "a record is copied in 16-byte units");
@@ -114,6 +115,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
                "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+               "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
                : "memory");
 }
 template <int N> __device__ __forceinline__ void reg_alloc() {
@@ -197,7 +203,7 @@ template <int KD> struct __align__(1024) PrepSmem {
   };
   f2 g[kC];  // running sum of log2 of the decays, hi and lo
   float beta[kC], f[kC], h[kC], qq[kC];
-  float bkn[2], tn[4];
+  float bkn[2], bvn[2], tn[4];
   uint64_t full, done;
   uint32_t taddr;
 };
@@ -405,7 +411,11 @@ __global__ void __launch_bounds__(kPrepThreads)
   if (on) {
     f = pow2i(-e);
     nf = pow2i(e);
-    if (p.flags & GDR_QK_L2NORM) nf = n2 == 0.f ? 0.f : nf / sqrtf(n2 + p.l2_eps);
+    if (p.flags & GDR_QK_L2NORM) {
+      const float a = n2 + p.l2_eps, r = rsqrtf(a);
+      // (one Newton step on the hardware's; infinite norms give 0)
+      nf = n2 == 0.f || !(r > 0.f) ? 0.f : nf * (r * fmaf(-0.5f * a * r, r, 1.5f));
+    }
     if (n2 != n2) nf = n2;
   }
   const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
@@ -421,8 +431,11 @@ __global__ void __launch_bounds__(kPrepThreads)
     fac[5 * kC + tok] = f;                                          // fk
     s.f[tok] = f;
     s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
-    const float m = warp_max(2.f * fabsf(nb * eg));
-    if (lane == 0) s.bkn[pw] = m;
+    const float m = warp_max(2.f * fabsf(nb * eg)), mv = warp_max(fabsf(nf * b));
+    if (lane == 0) {
+      s.bkn[pw] = m;
+      s.bvn[pw] = mv;
+    }
   } else {
     const float cq = p.scale * nf;
     fac[3 * kC + tok] = cq * eg;  // cqe
@@ -571,7 +584,8 @@ __global__ void __launch_bounds__(kPrepThreads)
     fac[7 * kC] = gtot;
     fac[7 * kC + 1] = fmaxf(s.bkn[0], s.bkn[1]);
     fac[7 * kC + 2] = tn * sc.x;
-    fac[7 * kC + 3] = (float)eT;
+    fac[7 * kC + 3] = fmaxf(s.bvn[0], s.bvn[1]);
+    fac[7 * kC + 4] = (float)eT;
   }
   fence_async_smem();
   if (!ok && tp.status) atomicExch(tp.status, 1);
@@ -597,7 +611,8 @@ __global__ void __launch_bounds__(kPrepThreads)
 //   12-15  y from QS and PU, a chunk behind.
 //   16     copies of K and Q ([64 x 64] slabs, 128-byte swizzle, three stages).
 //   17     MMA issuer.
-//   18     copies of V ([64 x 128]) and the record (two stages).
+//   18     copies of the records (two stages).
+//   19     copies of V ([64 x 128], two stages).
 constexpr int kThreads = 640;
 // Registers a thread of the groups; together the launch's 640 x 96.
 constexpr int kRegChain = 160, kRegSide = 64, kRegIssue = 32;
@@ -615,7 +630,8 @@ template <int KD> struct __align__(1024) GdrSmem {
   // maxima, by lane quarter and half; of a chunk's y, the scales of QS and PU,
   // and a warp's factors with them
   float vmax[4][2], smax[4][2], ysc[2][4][2], yfac[4][2][kC];
-  uint64_t fullk[3], conv[3], empty[3], fullr[2], ofree[2], sready[2];
+  __align__(128) __nv_bfloat16 y[4][kC][32];  // a chunk's y, a warp's 32 columns
+  uint64_t fullk[3], conv[3], empty[3], fullr[2], ofree[2], fullv[2], vfree[2], sready[2];
   uint64_t ksdone, rready, udone, uready, supdone, pudone;
   uint32_t taddr;
 };
@@ -638,7 +654,8 @@ struct Waiter {
 template <int KD>
 __global__ void __launch_bounds__(kThreads, 1)
     gdr_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mQ,
-                  const __grid_constant__ CUtensorMap mV, const GdrTcParams tp) {
+                  const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mY,
+                  const GdrTcParams tp) {
   constexpr int NP = KD / 64;        // slabs
   constexpr int KH = KD / 2;         // key dimensions of a chain warp's half
   constexpr int KS16 = KD / 16;      // K steps over the key dimension
@@ -681,6 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.fullr[i], 1);
       mbar_init(&s.ofree[i], 4);
+      mbar_init(&s.fullv[i], 1);
+      mbar_init(&s.vfree[i], 8);
       mbar_init(&s.sready[i], 4);
     }
     mbar_init(&s.ksdone, 1);
@@ -722,20 +741,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Leave no copy in flight: the last chunks issued have landed.
       for (int i = c > 3 ? c - 3 : 0; i < c; ++i) mbar_wait(&s.fullk[i % 3], (i / 3) & 1, kWaitLimit);
     } else if (warp == 18 && lane == 0) {
-      // ---------------------------------------------------------- values and records
-      tma_prefetch_desc(&mV);
+      // ---------------------------------------------------------- records
       const uint8_t *rec = tp.rec + (first_slot(tp, seq, t0) * p.H + hd) * (int64_t)sizeof(Rec);
+      pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
         const int r2 = c & 1;
         if (c >= 2 && !mbar_wait(&s.ofree[r2], ((c >> 1) - 1) & 1, kWaitLimit)) break;
-        mbar_expect_tx(&s.fullr[r2], kC * kV * 2 + (uint32_t)sizeof(Rec));
-        tma_load_3d(s.v[r2], &mV, &s.fullr[r2], (int)v0, (int)hd, (int)(t0 + (int64_t)c * kC));
-        if (c == 0) pdl_wait();  // the records
+        mbar_expect_tx(&s.fullr[r2], (uint32_t)sizeof(Rec));
         bulk_load(&s.rec[r2].r, rec + c * p.H * (int64_t)sizeof(Rec), sizeof(Rec), &s.fullr[r2]);
       }
       if (c < nch && tp.status) atomicExch(tp.status, 2);
       for (int i = c > 2 ? c - 2 : 0; i < c; ++i) mbar_wait(&s.fullr[i & 1], (i >> 1) & 1, kWaitLimit);
+    } else if (warp == 19 && lane == 0) {
+      // ---------------------------------------------------------- values
+      tma_prefetch_desc(&mV);
+      int c = 0;
+      for (; c < nch; ++c) {
+        const int r2 = c & 1;
+        if (c >= 2 && !mbar_wait(&s.vfree[r2], ((c >> 1) - 1) & 1, kWaitLimit)) break;
+        mbar_expect_tx(&s.fullv[r2], kC * kV * 2);
+        tma_load_3d(s.v[r2], &mV, &s.fullv[r2], (int)v0, (int)hd, (int)(t0 + (int64_t)c * kC));
+      }
+      if (c < nch && tp.status) atomicExch(tp.status, 2);
+      for (int i = c > 2 ? c - 2 : 0; i < c; ++i) mbar_wait(&s.fullv[i & 1], (i >> 1) & 1, kWaitLimit);
     } else if (warp == 17) {
       // ---------------------------------------------------------- MMA issuer
       const bool leader = elect_one();
@@ -751,9 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // K step kk of a K-major operand of two slabs, in descriptor units
       auto koff = [](int kk) { return (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4); };
-      // TMEM column of K step kk of S's hi pieces (lo: KH / 2 further on)
-      auto scol = [](int kk) { return kColS + (kk / (KH / 16)) * KH + (kk % (KH / 16)) * 8; };
-      // of K step kk of R, U and U' (lo: 16 further on)
+      // TMEM column of K step kk of S's, R's, U's hi pieces: 32 columns hold hi
+      // and, 16 further on, lo of 32 values
       auto rcol = [](int kk) { return 32 * (kk >> 1) + 8 * (kk & 1); };
       for (int c = 0; c < nch; ++c) {
         const uint32_t ph = c & 1, php = (c - 1) & 1;
@@ -774,22 +802,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 0; x < 2; ++x)
 #pragma unroll
               for (int kk = h * (KS16 / 2); kk < (h + 1) * (KS16 / 2); ++kk)
-                mma_ts(tb + kColKS, tb + scol(kk) + x * (KH / 2), dk + koff(kk), id64, h + x + kk > 0);
+                mma_ts(tb + kColKS, tb + kColS + rcol(kk) + x * 16, dk + koff(kk), id64, h + x + kk > 0);
           }
           __syncwarp();
         }
         if (wait.dead) break;
         commit(&s.ksdone, ph);
-        // QS and PU of the chunk before have been read
-        if (c > 0) wait(&s.ofree[php], ((c - 1) >> 1) & 1, 5);
-        if (wait.dead) break;
-        tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < KS16; ++kk)
-            mma_ts(tb + kColQS, tb + scol(kk), dq + koff(kk), id64, kk > 0);
-        }
-        __syncwarp();
         wait(&s.fullr[ph], (c >> 1) & 1, 6);
         wait(&s.rready, ph, 7);
         if (wait.dead) break;
@@ -803,6 +821,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (x == 2 ? tl : th) + 2 * kk, id64, x + kk > 0);
         }
         commit(&s.udone, ph);
+        // QS and PU of the chunk before have been read
+        if (c > 0) wait(&s.ofree[php], ((c - 1) >> 1) & 1, 5);
+        if (wait.dead) break;
+        tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < KS16; ++kk)
+            mma_ts(tb + kColQS, tb + kColS + rcol(kk), dq + koff(kk), id64, kk > 0);
+        }
+        __syncwarp();
         wait(&s.uready, ph, 8);
         if (wait.dead) break;
         tc_fence_after();
@@ -846,7 +874,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         yf[1][lane + 32 * e] = rc.cqp[lane + 32 * e] * fP;
       }
       __syncwarp();
+      // a whole chunk leaves by TMA (columns behind V are not written), the
+      // last one's rows one by one
+      const bool whole = nv == kC;
       __nv_bfloat16 *yp = yb + (int64_t)c * kC * yrow;
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         uint32_t r[16], u[16], out[8];
@@ -867,12 +900,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             out[2 * q + e] = pack_bf16x2(o.x, o.y);
           }
         }
-        if (live && 16 * i + 16 <= nv) {
+        if (whole) {
+          uint16_t *sy = reinterpret_cast<uint16_t *>(&s.y[quarter][16 * i][lane]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            *reinterpret_cast<uint16_t *>(yp) = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
-            yp += yrow;
-          }
+          for (int j = 0; j < 16; ++j) sy[32 * j] = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
         } else if (live) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -882,9 +913,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
+      if (whole) fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.ofree[par]);
+      if (lane == 0) {
+        mbar_arrive(&s.ofree[par]);
+        if (whole && v0 + 32 * quarter < p.V) {
+          tma_store_3d(&mY, s.y[quarter], (int)v0 + 32 * quarter, (int)hd, (int)(t0 + (int64_t)c * kC));
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------ conversion
     reg_dealloc<kRegSide>();
@@ -932,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pair_sync(quarter);
     float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
     int eS = scale_exp(smax);
-    // S's pieces, hi and lo of each half within the half's own dS columns
+    // S's pieces, hi and lo of 32 values within their own dS columns
     const uint32_t mycol = tb + lane_base + kColS + ch * KH;
     {
       const f2 sc = mk2(pow2i(eS), pow2i(eS));
@@ -944,8 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           st[16 * i + j] = mul2(st[16 * i + j], sc);
           split_h2(st[16 * i + j], hi[j], lo[j]);
         }
-        tmem_st16(mycol + 16 * i, hi);
-        tmem_st16(mycol + KH / 2 + 16 * i, lo);
+        tmem_st16(mycol + 32 * i, hi);
+        tmem_st16(mycol + 32 * i + 16, lo);
       }
     }
     tmem_st_wait();
@@ -953,32 +993,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sready[ch]);
 
-    // b v of chunk c, and its maximum
-    f2 x[16];
+    // The values of chunk c, two tokens a register, and their maximum.
+    uint32_t vv[16];
     auto values = [&](int c) {
       const int par = c & 1;
-      const int64_t left = len - (int64_t)c * kC;
-      const int nv = (int)(left < kC ? left : kC);
-      const Rec &rc = s.rec[par].r;
-      wait(&s.fullr[par], (c >> 1) & 1, 13);
-      float m = 0.f;
+      const int64_t left = len - (int64_t)c * kC - 32 * ch;
+      const int nv = (int)(left < 32 ? left : 32);
+      wait(&s.fullv[par], (c >> 1) & 1, 13);
+      const uint16_t *vp = reinterpret_cast<const uint16_t *>(&s.v[par][32 * ch][cv]);
+      uint16_t v[32];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int j = 32 * ch + 4 * q;
-        const float4 bv = *reinterpret_cast<const float4 *>(&rc.bv[j]);
-        float v[4];
+      for (int j = 0; j < 32; ++j) v[j] = vp[j * kV];
+      __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __bfloat162float(s.v[par][j + e][cv]);
-        if (nv < kC) {  // rows behind the end may hold anything
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + e >= nv) v[e] = 0.f;
+      for (int q = 0; q < 16; ++q) {
+        vv[q] = (uint32_t)v[2 * q] | ((uint32_t)v[2 * q + 1] << 16);
+        if (nv < 32) {  // rows behind the end may hold anything
+          if (2 * q >= nv) vv[q] = 0u;
+          else if (2 * q + 1 >= nv) vv[q] &= 0xffffu;
         }
-        x[2 * q] = mul2(mk2(bv.x, bv.y), mk2(v[0], v[1]));
-        x[2 * q + 1] = mul2(mk2(bv.z, bv.w), mk2(v[2], v[3]));
-        m = fmaxf(fmaxf(m, fabsf(x[2 * q].x)), fabsf(x[2 * q].y));
-        m = fmaxf(fmaxf(m, fabsf(x[2 * q + 1].x)), fabsf(x[2 * q + 1].y));
+        m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vv[q])));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.vfree[par]);
+      float m = fmaxf(__low2float(m2), __high2float(m2));
       m = warp_max(m);
       if (lane == 0) s.vmax[quarter][ch] = m;
     };
@@ -990,24 +1028,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // While KS runs: the chunk's scales.  |R| <= bR, |U| <= |T| bR row by
       // row, |dS| <= sum |k| |U| <= 128 max |U|: R and U take one scale, U' the
       // next state's, so that dS comes out in it.
+      wait(&s.fullr[par], (c >> 1) & 1, 17);
       pair_sync(quarter);
       if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
       const float gC = rc.gC;
       const int eT = (int)rc.eT;
       const float tn = rc.tn * pow2i(-eT);
-      const float bR = fmaxf(s.vmax[quarter][0], s.vmax[quarter][1]) + rc.bkn * kNorm * smax;
+      const float bR = fmaxf(s.vmax[quarter][0], s.vmax[quarter][1]) * rc.bvn + rc.bkn * kNorm * smax;
       const int eR = scale_exp(bR * fmaxf(tn, 1.f));
       const int eN = scale_exp(fabsf(gC) * smax + 128.f * (tn * bR));
-      f2 nb[16];
+      f2 x[16], nb[16];  // of R: b v, and the factors of KS
       {
         const f2 fR = mk2(pow2i(eR), pow2i(eR)), fK = mk2(-pow2i(-eS), -pow2i(-eS));
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
+          const float4 bv = *reinterpret_cast<const float4 *>(&rc.bv[32 * ch + 4 * q]);
           const float4 bk = *reinterpret_cast<const float4 *>(&rc.bk[32 * ch + 4 * q]);
-          x[2 * q] = mul2(x[2 * q], fR);
-          x[2 * q + 1] = mul2(x[2 * q + 1], fR);
-          nb[2 * q] = mul2(mul2(mk2(bk.x, bk.y), fK), fR);
-          nb[2 * q + 1] = mul2(mul2(mk2(bk.z, bk.w), fK), fR);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t w = vv[2 * q + e];
+            x[2 * q + e] = mul2(mul2(e ? mk2(bv.z, bv.w) : mk2(bv.x, bv.y), fR), mk2(bf16lo(w), bf16hi(w)));
+            nb[2 * q + e] = mul2(mul2(e ? mk2(bk.z, bk.w) : mk2(bk.x, bk.y), fK), fR);
+          }
         }
       }
       if (ch == 0 && lane == 0) {
@@ -1075,9 +1117,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float gn = gC * pow2i(eN - eS);  // (the difference beyond the range: all or nothing is left)
         const f2 g2 = mk2(gn, gn);
         eS = eN;
-        uint32_t r[2][16], hi[KH / 2], lo[KH / 2], mh = 0u;
+        uint32_t mh = 0u;
 #pragma unroll
         for (int i = 0; i < KH / 32; ++i) {
+          uint32_t r[2][16], hi[16], lo[16];
           tmem_ld16(mycol + 32 * i, r[0]);
           tmem_ld16(mycol + 32 * i + 16, r[1]);
           tmem_ld_wait();
@@ -1086,15 +1129,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2 &v = st[16 * i + j];
             const uint32_t a = r[j >> 3][2 * (j & 7)], b = r[j >> 3][2 * (j & 7) + 1];
             v = fma2(v, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
-            split_h2(v, hi[16 * i + j], lo[16 * i + j]);
-            mh = maxabs_h2(mh, hi[16 * i + j]);
+            split_h2(v, hi[j], lo[j]);
+            mh = maxabs_h2(mh, hi[j]);
           }
-        }
-        // (this warp's own dS columns, all read)
-#pragma unroll
-        for (int i = 0; i < KH / 32; ++i) {
-          tmem_st16(mycol + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(&hi[16 * i]));
-          tmem_st16(mycol + KH / 2 + 16 * i, *reinterpret_cast<const uint32_t(*)[16]>(&lo[16 * i]));
+          tmem_st16(mycol + 32 * i, hi);
+          tmem_st16(mycol + 32 * i + 16, lo);
         }
         const uint32_t a = mh & 0x7fffu, b = (mh >> 16) & 0x7fffu;  // float16 order is that of the bits
         mh = a > b ? a : b;
@@ -1139,7 +1178,7 @@ int64_t slots_of(const GdrParams &p) {
 
 template <int KD>
 cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMap &mQ,
-                   const CUtensorMap &mV, cudaStream_t s) {
+                   const CUtensorMap &mV, const CUtensorMap &mY, cudaStream_t s) {
   const size_t prep = sizeof(PrepSmem<KD>) + 1024, smem = sizeof(GdrSmem<KD>) + 1024;
   // (set on every call: the attribute belongs to the current device)
   cudaError_t e = cudaFuncSetAttribute(gdr_prep_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1151,7 +1190,7 @@ cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMa
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(gdr_tc_kernel<KD>, dim3((unsigned)(q.p.nseq * q.p.H * q.vtiles)),
-                          dim3(kThreads), smem, s, mK, mQ, mV, q);
+                          dim3(kThreads), smem, s, mK, mQ, mV, mY, q);
 }
 
 }  // namespace
@@ -1174,14 +1213,15 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   q.chunks = p.cu ? 0 : (p.L + kC - 1) / kC;
   q.rec = static_cast<uint8_t *>(workspace) + kGdrStatusBytes;
   q.status = static_cast<int *>(workspace);
-  CUtensorMap mK, mQ, mV;
+  CUtensorMap mK, mQ, mV, mY;
   if (!encode(&mK, p.k, p.K, p.Hk, p.rows, p.k_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&mQ, p.q, p.K, p.Hk, p.rows, p.q_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode(&mV, p.v, p.V, p.H, p.rows, p.v_row, kV, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !encode(&mV, p.v, p.V, p.H, p.rows, p.v_row, kV, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode(&mY, p.y, p.V, p.H, p.rows, p.H * p.V, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaMemsetAsync(q.status, 0, sizeof(int), s);
   if (e != cudaSuccess) return e;
-  return p.K <= 64 ? launch<64>(q, mK, mQ, mV, s) : launch<128>(q, mK, mQ, mV, s);
+  return p.K <= 64 ? launch<64>(q, mK, mQ, mV, mY, s) : launch<128>(q, mK, mQ, mV, mY, s);
 }
 
 }  // namespace ssm
