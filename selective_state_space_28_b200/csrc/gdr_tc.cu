@@ -66,14 +66,13 @@ constexpr int kAm = 68;   // row stride of A / T in float32 (a row a lane: no ba
 struct Rec {
   uint8_t T[2][kC * 128];  // hi, lo: 64 x 64 float16, 128-byte swizzled rows
   uint8_t P[kC * 128];
-  float bv[kC], bk[kC], cu[kC], cqe[kC], cqp[kC];  // factors of V, KS, U', QS, PU
-  float fk[kC], fq[kC];                            // powers of two of keys and queries
-  // e^g_63; bounds of bk |k|, of T's rows (scaled), of bv; T's exponent
-  float gC, bkn, tn, bvn, eT;
-  float pad[11];
+  float ek[kC], cu[kC], cq[kC];  // factors of KS (negative), U' and y
+  float fk[kC], fq[kC], eg[kC];  // of keys and queries: powers of two; decays of queries
+  float gC, ekn, tn, eT;         // e^g_63; bounds of ek |k| and of T's rows (scaled); T's exponent
+  float pad[12];
 };
 constexpr size_t kRecT = 2 * kC * 128;
-static_assert(sizeof(Rec) == 26432 && sizeof(Rec) % 16 == 0, "a record is copied in 16-byte units");
+static_assert(sizeof(Rec) == 26176 && sizeof(Rec) % 16 == 0, "a record is copied in 16-byte units");
 
 struct GdrTcParams {
   GdrParams p;
@@ -158,6 +157,16 @@ __device__ __forceinline__ uint32_t maxabs_h2(uint32_t a, uint32_t b) {
   asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t maxabs_bf2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float fma_bf16(uint16_t x, uint16_t y, float c) {
+  float d;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
+  return d;
+}
 // Two bfloat16 times a bfloat16, plus c, in float32.
 __device__ __forceinline__ f2 fma_bf16x2(uint32_t x, uint32_t y, f2 c) {
   f2 d;
@@ -202,8 +211,8 @@ template <int KD> struct __align__(1024) PrepSmem {
     };
   };
   f2 g[kC];  // running sum of log2 of the decays, hi and lo
-  float beta[kC], f[kC], h[kC], qq[kC];
-  float bkn[2], bvn[2], tn[4];
+  float beta[kC], f[kC], h[kC], qq[kC], bv[kC];
+  float ekn[2], tn[4];
   uint64_t full, done;
   uint32_t taddr;
 };
@@ -213,7 +222,7 @@ template <int KD> struct __align__(1024) PrepSmem {
 // lane layout.
 __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // 11 bits, to nearest
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -229,7 +238,7 @@ __device__ __forceinline__ void small_product(const float *a, const float *b, fl
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[m][e] = 0.f;
-#pragma unroll
+#pragma unroll 1  // (short code: several CTAs share the instruction cache)
   for (int k = 0; k < KT; ++k) {
     uint32_t bh[2], bl[2];
 #pragma unroll
@@ -420,27 +429,23 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
   const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
   const float eg = ex2(gi.x + gi.y);
-  float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, bv) - kRecT));
+  float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, ek) - kRecT));
   float rowf = f;
   if (isk) {
-    const float b = s.beta[tok], nb = nf * nf * b;
-    rowf = nb * f;
-    fac[0 * kC + tok] = nf * b;                                     // bv
-    fac[1 * kC + tok] = nb * eg;                                    // bk
-    fac[2 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));       // cu
-    fac[5 * kC + tok] = f;                                          // fk
+    const float b = s.beta[tok];
+    rowf = nf * nf * b * f;
+    s.bv[tok] = nf * b;
+    fac[0 * kC + tok] = -nf * eg;                              // ek
+    fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
+    fac[3 * kC + tok] = f;                                     // fk
     s.f[tok] = f;
     s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
-    const float m = warp_max(2.f * fabsf(nb * eg)), mv = warp_max(fabsf(nf * b));
-    if (lane == 0) {
-      s.bkn[pw] = m;
-      s.bvn[pw] = mv;
-    }
+    const float m = warp_max(2.f * nf * eg);
+    if (lane == 0) s.ekn[pw] = m;
   } else {
-    const float cq = p.scale * nf;
-    fac[3 * kC + tok] = cq * eg;  // cqe
-    fac[4 * kC + tok] = cq;       // cqp
-    fac[6 * kC + tok] = f;        // fq
+    fac[2 * kC + tok] = p.scale * nf;  // cq
+    fac[4 * kC + tok] = f;             // fq
+    fac[5 * kC + tok] = eg;
   }
   __syncthreads();  // f, h
 
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
   }
   __syncthreads();
-  // T to float16 pairs: row pt / 2, half pt % 2
+  // T diag(b) to float16 pairs: row pt / 2, half pt % 2
   const int row = pt >> 1, hf = pt & 1;
   const bool have = hf <= (row >> 5);
   f2 t[16];
@@ -558,9 +563,10 @@ __global__ void __launch_bounds__(kPrepThreads)
   for (int q = 0; q < 8; ++q) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     if (have) a = *reinterpret_cast<const float4 *>(&s.Am[row][32 * hf + 4 * q]);
-    t[2 * q] = mk2(a.x, a.y);
-    t[2 * q + 1] = mk2(a.z, a.w);
-    sum += (fabsf(a.x) + fabsf(a.y)) + (fabsf(a.z) + fabsf(a.w));
+    const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
+    t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
+    t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
+    sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
   }
   sum += __shfl_xor_sync(0xffffffffu, sum, 1);
   sum = warp_max(sum);
@@ -581,11 +587,10 @@ __global__ void __launch_bounds__(kPrepThreads)
     *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
   }
   if (pw == 3 && lane == 0) {
-    fac[7 * kC] = gtot;
-    fac[7 * kC + 1] = fmaxf(s.bkn[0], s.bkn[1]);
-    fac[7 * kC + 2] = tn * sc.x;
-    fac[7 * kC + 3] = fmaxf(s.bvn[0], s.bvn[1]);
-    fac[7 * kC + 4] = (float)eT;
+    fac[6 * kC] = gtot;
+    fac[6 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
+    fac[6 * kC + 2] = tn * sc.x;
+    fac[6 * kC + 3] = (float)eT;
   }
   fence_async_smem();
   if (!ok && tp.status) atomicExch(tp.status, 1);
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 //   12-15  y from QS and PU, a chunk behind.
 //   16     copies of K and Q ([64 x 64] slabs, 128-byte swizzle, three stages).
 //   17     MMA issuer.
-//   18     copies of the records (two stages).
+//   18     copies of the records (three stages).
 //   19     copies of V ([64 x 128], two stages).
 constexpr int kThreads = 640;
 // Registers a thread of the groups; together the launch's 640 x 96.
@@ -621,17 +626,17 @@ static_assert(256 * kRegChain + 256 * kRegSide + 128 * kRegIssue <= kThreads * 9
 // TMEM columns.  dS lands where S's pieces are (they are rewritten from it),
 // the product with T where KS was, U's hi parts where R's pieces were.
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColKS = 128, kColQS = 192, kColR = 256, kColU2 = 320, kColPU = 384;
+constexpr uint32_t kColS = 0, kColKS = 128, kColR = 192, kColU2 = 256, kColY = 320;  // Y: two
 
 template <int KD> struct __align__(1024) GdrSmem {
   uint8_t kq[3][KD / 64][128 * 128];  // [stage][slab]: rows 0-63 keys, 64-127 queries
   __nv_bfloat16 v[2][kC][kV];
-  struct __align__(1024) { Rec r; } rec[2];
-  // maxima, by lane quarter and half; of a chunk's y, the scales of QS and PU,
-  // and a warp's factors with them
-  float vmax[4][2], smax[4][2], ysc[2][4][2], yfac[4][2][kC];
-  __align__(128) __nv_bfloat16 y[4][kC][32];  // a chunk's y, a warp's 32 columns
-  uint64_t fullk[3], conv[3], empty[3], fullr[2], ofree[2], fullv[2], vfree[2], sready[2];
+  struct __align__(1024) { Rec r; } rec[3];
+  __align__(128) __nv_bfloat16 y[4][kC / 2][32];  // half a chunk's y, a warp's 32 columns
+  // maxima, by lane quarter (and half); of a chunk's y, the scale, and a warp's
+  // factors with it
+  float vmax[2][4], smax[4][2], ysc[3][4], yfac[4][kC];
+  uint64_t fullk[3], conv[3], empty[3], fullr[3], rfree[3], yfree[2], fullv[2], vfree[2], sready[2];
   uint64_t ksdone, rready, udone, uready, supdone, pudone;
   uint32_t taddr;
 };
@@ -694,10 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.fullk[i], 1);
       mbar_init(&s.conv[i], 4);
       mbar_init(&s.empty[i], 1);
+      mbar_init(&s.fullr[i], 1);
+      mbar_init(&s.rfree[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.fullr[i], 1);
-      mbar_init(&s.ofree[i], 4);
+      mbar_init(&s.yfree[i], 4);
       mbar_init(&s.fullv[i], 1);
       mbar_init(&s.vfree[i], 8);
       mbar_init(&s.sready[i], 4);
@@ -746,13 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
-        const int r2 = c & 1;
-        if (c >= 2 && !mbar_wait(&s.ofree[r2], ((c >> 1) - 1) & 1, kWaitLimit)) break;
-        mbar_expect_tx(&s.fullr[r2], (uint32_t)sizeof(Rec));
-        bulk_load(&s.rec[r2].r, rec + c * p.H * (int64_t)sizeof(Rec), sizeof(Rec), &s.fullr[r2]);
+        const int r3 = c % 3;
+        if (c >= 3 && !mbar_wait(&s.rfree[r3], (c / 3 - 1) & 1, kWaitLimit)) break;
+        mbar_expect_tx(&s.fullr[r3], (uint32_t)sizeof(Rec));
+        bulk_load(&s.rec[r3].r, rec + c * p.H * (int64_t)sizeof(Rec), sizeof(Rec), &s.fullr[r3]);
       }
       if (c < nch && tp.status) atomicExch(tp.status, 2);
-      for (int i = c > 2 ? c - 2 : 0; i < c; ++i) mbar_wait(&s.fullr[i & 1], (i >> 1) & 1, kWaitLimit);
+      for (int i = c > 3 ? c - 3 : 0; i < c; ++i) mbar_wait(&s.fullr[i % 3], (i / 3) & 1, kWaitLimit);
     } else if (warp == 19 && lane == 0) {
       // ---------------------------------------------------------- values
       tma_prefetch_desc(&mV);
@@ -784,13 +790,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and, 16 further on, lo of 32 values
       auto rcol = [](int kk) { return 32 * (kk >> 1) + 8 * (kk & 1); };
       for (int c = 0; c < nch; ++c) {
-        const uint32_t ph = c & 1, php = (c - 1) & 1;
+        const uint32_t ph = c & 1, ycol = tb + kColY + 64 * ph;
         const uint64_t dk = smem_desc(smem_u32(s.kq[c % 3][0]), 16, 1024, kSwizzle128B);
         const uint64_t dq = dk + ((kC * 128) >> 4);
         const uint64_t dm = smem_desc(smem_u32(s.kq[c % 3][0]), 128 * 128, 1024, kSwizzle128B);
-        const uint64_t th = smem_desc(smem_u32(s.rec[ph].r.T[0]), 16, 1024, kSwizzle128B);
-        const uint64_t tl = smem_desc(smem_u32(s.rec[ph].r.T[1]), 16, 1024, kSwizzle128B);
-        const uint64_t dp = smem_desc(smem_u32(s.rec[ph].r.P), 16, 1024, kSwizzle128B);
+        const uint64_t th = smem_desc(smem_u32(s.rec[c % 3].r.T[0]), 16, 1024, kSwizzle128B);
+        const uint64_t tl = smem_desc(smem_u32(s.rec[c % 3].r.T[1]), 16, 1024, kSwizzle128B);
+        const uint64_t dp = smem_desc(smem_u32(s.rec[c % 3].r.P), 16, 1024, kSwizzle128B);
         wait(&s.conv[c % 3], (c / 3) & 1, 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // a half of the state at a time
@@ -808,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (wait.dead) break;
         commit(&s.ksdone, ph);
-        wait(&s.fullr[ph], (c >> 1) & 1, 6);
+        wait(&s.fullr[c % 3], (c / 3) & 1, 6);
         wait(&s.rready, ph, 7);
         if (wait.dead) break;
         tc_fence_after();
@@ -821,14 +827,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (x == 2 ? tl : th) + 2 * kk, id64, x + kk > 0);
         }
         commit(&s.udone, ph);
-        // QS and PU of the chunk before have been read
-        if (c > 0) wait(&s.ofree[php], ((c - 1) >> 1) & 1, 5);
+        // y of the chunk two before has been read
+        if (c > 1) wait(&s.yfree[ph], ((c >> 1) - 1) & 1, 5);
         if (wait.dead) break;
         tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < KS16; ++kk)
-            mma_ts(tb + kColQS, tb + kColS + rcol(kk), dq + koff(kk), id64, kk > 0);
+            mma_ts(ycol, tb + kColS + rcol(kk), dq + koff(kk), id64, kk > 0);
         }
         __syncwarp();
         wait(&s.uready, ph, 8);
@@ -844,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit(&s.empty[c % 3]);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tb + kColPU, tb + kColR + rcol(kk), dp + 2 * kk, id64, kk > 0);
+            mma_ts(ycol, tb + kColR + rcol(kk), dp + 2 * kk, id64, 1);
         }
         commit(&s.pudone, ph);
       }
@@ -861,49 +867,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int par = c & 1;
       const int64_t left = len - (int64_t)c * kC;
       const int nv = (int)(left < kC ? left : kC);
-      const Rec &rc = s.rec[par].r;
-      wait(&s.fullr[par], (c >> 1) & 1, 9);
+      const Rec &rc = s.rec[c % 3].r;
+      wait(&s.fullr[c % 3], (c / 3) & 1, 9);
       wait(&s.pudone, par, 10);
       tc_fence_after();
       // this warp's factors of the tokens
-      const float fQ = s.ysc[par][quarter][0], fP = s.ysc[par][quarter][1];
-      float(*yf)[kC] = s.yfac[quarter];
+      float *yf = s.yfac[quarter];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        yf[0][lane + 32 * e] = rc.cqe[lane + 32 * e] * fQ;
-        yf[1][lane + 32 * e] = rc.cqp[lane + 32 * e] * fP;
-      }
+      for (int e = 0; e < 2; ++e) yf[lane + 32 * e] = rc.cq[lane + 32 * e] * s.ysc[c % 3][quarter];
       __syncwarp();
+      if (lane == 0) mbar_arrive(&s.rfree[c % 3]);
       // a whole chunk leaves by TMA (columns behind V are not written), the
       // last one's rows one by one
       const bool whole = nv == kC;
       __nv_bfloat16 *yp = yb + (int64_t)c * kC * yrow;
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
-        uint32_t r[16], u[16], out[8];
-        tmem_ld16(tb + lane_base + kColQS + 16 * i, r);
-        tmem_ld16(tb + lane_base + kColPU + 16 * i, u);
+        uint32_t r[16], out[8];
+        tmem_ld16(tb + lane_base + kColY + 64 * par + 16 * i, r);
+        if (whole && !(i & 1)) {  // the half before has left
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
         tmem_ld_wait();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 ce = *reinterpret_cast<const float4 *>(&yf[0][16 * i + 4 * q]);
-          const float4 cp = *reinterpret_cast<const float4 *>(&yf[1][16 * i + 4 * q]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = 4 * q + 2 * e;
-            const f2 qs = mk2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-            const f2 pu = mk2(__uint_as_float(u[k]), __uint_as_float(u[k + 1]));
-            const f2 o = fma2(e ? mk2(ce.z, ce.w) : mk2(ce.x, ce.y), qs,
-                              mul2(e ? mk2(cp.z, cp.w) : mk2(cp.x, cp.y), pu));
-            out[2 * q + e] = pack_bf16x2(o.x, o.y);
-          }
+          const float4 f = *reinterpret_cast<const float4 *>(&yf[16 * i + 4 * q]);
+          const f2 o0 = mul2(mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])), mk2(f.x, f.y));
+          const f2 o1 = mul2(mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])), mk2(f.z, f.w));
+          out[2 * q] = pack_bf16x2(o0.x, o0.y);
+          out[2 * q + 1] = pack_bf16x2(o1.x, o1.y);
         }
         if (whole) {
-          uint16_t *sy = reinterpret_cast<uint16_t *>(&s.y[quarter][16 * i][lane]);
+          uint16_t *sy = reinterpret_cast<uint16_t *>(&s.y[quarter][16 * (i & 1)][lane]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) sy[32 * j] = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
+          if (i & 1) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && v0 + 32 * quarter < p.V) {
+              tma_store_3d(&mY, s.y[quarter], (int)v0 + 32 * quarter, (int)hd,
+                           (int)(t0 + (int64_t)c * kC + 16 * (i - 1)));
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+          }
         } else if (live) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -913,15 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      if (whole) fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.ofree[par]);
-        if (whole && v0 + 32 * quarter < p.V) {
-          tma_store_3d(&mY, s.y[quarter], (int)v0 + 32 * quarter, (int)hd, (int)(t0 + (int64_t)c * kC));
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
-      }
+      if (lane == 0) mbar_arrive(&s.yfree[par]);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
@@ -930,10 +930,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dealloc<kRegSide>();
     const int pt = tid - 256, tok = pt & 63;
     for (int c = 0; c < nch; ++c) {
-      const int par = c & 1;
       const int64_t left = len - (int64_t)c * kC;
-      wait(&s.fullr[par], (c >> 1) & 1, 11);
-      const float f = pt < 64 ? s.rec[par].r.fk[tok] : s.rec[par].r.fq[tok];
+      const Rec &rc = s.rec[c % 3].r;
+      {  // the largest finite value of this warp's quarter of V
+        wait(&s.fullv[c & 1], (c >> 1) & 1, 18);
+        const uint4 *vp = reinterpret_cast<const uint4 *>(&s.v[c & 1][lane >> 2][32 * quarter + 8 * (lane & 3)]);
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (8 * i + (lane >> 2) < left) {
+            const uint4 u = vp[i * (8 * kV / 8)];
+            m = maxabs_bf2(maxabs_bf2(m, u.x), maxabs_bf2(u.y, maxabs_bf2(u.z, u.w)));
+          }
+        }
+        float mx = fmaxf(fabsf(bf16lo(m)), fabsf(bf16hi(m)));
+        if (mx >= __uint_as_float(0x7f800000u)) {  // an infinity among them: look again
+          mx = 0.f;
+          const __nv_bfloat16 *ve = reinterpret_cast<const __nv_bfloat16 *>(vp);
+          for (int i = 0; i < 8; ++i)
+            for (int e = 0; e < 8; ++e) {
+              const float x = fabsf(__bfloat162float(ve[i * 8 * kV + e]));
+              if (8 * i + (lane >> 2) < left && x < __uint_as_float(0x7f800000u)) mx = fmaxf(mx, x);
+            }
+        }
+        mx = warp_max(mx);
+        if (lane == 0) s.vmax[c & 1][quarter] = mx;
+      }
+      wait(&s.fullr[c % 3], (c / 3) & 1, 11);
+      const float f = pt < 64 ? rc.fk[tok] : rc.fq[tok];
+      const float eg = pt < 64 ? 1.f : rc.eg[tok];
       const uint32_t f2x = __byte_perm(__float_as_uint(f), 0, 0x3232);  // (a power of two: exact)
       wait(&s.fullk[c % 3], (c / 3) & 1, 12);
       uint8_t *base = &s.kq[c % 3][0][0];
@@ -945,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
+          f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
+          if (pt >= 64) y = mul2(y, mk2(eg, eg));
           w[x] = on ? pack_h2(y.x, y.y) : 0u;
         }
         *at = make_uint4(w[0], w[1], w[2], w[3]);
@@ -971,7 +997,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) s.smax[quarter][ch] = m;
     pair_sync(quarter);
     float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
-    int eS = scale_exp(smax);
+    // One scale 2^e a chunk for S, R and U.  |R| <= max |v| + |ek k| sqrt(K)
+    // max |S|, |U| <= (T's row sums) max |R|, |dS| <= sum |k| |U'| <= 128 max |U|.
+    auto bound_R = [&](int c, float smax) {
+      return s.vmax[c & 1][quarter] + s.rec[c % 3].r.ekn * kNorm * smax;
+    };
+    auto row_sum = [&](int c) { return s.rec[c % 3].r.tn * pow2i(-(int)s.rec[c % 3].r.eT); };
+    wait(&s.fullr[0], 0, 13);
+    wait(&s.conv[0], 0, 13);
+    int eS = scale_exp(fmaxf(smax, fmaxf(1.f, row_sum(0)) * bound_R(0, smax)));
     // S's pieces, hi and lo of 32 values within their own dS columns
     const uint32_t mycol = tb + lane_base + kColS + ch * KH;
     {
@@ -993,69 +1027,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sready[ch]);
 
-    // The values of chunk c, two tokens a register, and their maximum.
-    uint32_t vv[16];
-    auto values = [&](int c) {
-      const int par = c & 1;
-      const int64_t left = len - (int64_t)c * kC - 32 * ch;
-      const int nv = (int)(left < 32 ? left : 32);
-      wait(&s.fullv[par], (c >> 1) & 1, 13);
-      const uint16_t *vp = reinterpret_cast<const uint16_t *>(&s.v[par][32 * ch][cv]);
-      uint16_t v[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = vp[j * kV];
-      __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        vv[q] = (uint32_t)v[2 * q] | ((uint32_t)v[2 * q + 1] << 16);
-        if (nv < 32) {  // rows behind the end may hold anything
-          if (2 * q >= nv) vv[q] = 0u;
-          else if (2 * q + 1 >= nv) vv[q] &= 0xffffu;
-        }
-        m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&vv[q])));
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.vfree[par]);
-      float m = fmaxf(__low2float(m2), __high2float(m2));
-      m = warp_max(m);
-      if (lane == 0) s.vmax[quarter][ch] = m;
-    };
-    values(0);
     for (int c = 0; c < nch; ++c) {
       const int par = c & 1;
       const uint32_t ph = par;
-      const Rec &rc = s.rec[par].r;
-      // While KS runs: the chunk's scales.  |R| <= bR, |U| <= |T| bR row by
-      // row, |dS| <= sum |k| |U| <= 128 max |U|: R and U take one scale, U' the
-      // next state's, so that dS comes out in it.
-      wait(&s.fullr[par], (c >> 1) & 1, 17);
-      pair_sync(quarter);
-      if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
-      const float gC = rc.gC;
-      const int eT = (int)rc.eT;
-      const float tn = rc.tn * pow2i(-eT);
-      const float bR = fmaxf(s.vmax[quarter][0], s.vmax[quarter][1]) * rc.bvn + rc.bkn * kNorm * smax;
-      const int eR = scale_exp(bR * fmaxf(tn, 1.f));
-      const int eN = scale_exp(fabsf(gC) * smax + 128.f * (tn * bR));
-      f2 x[16], nb[16];  // of R: b v, and the factors of KS
+      const int64_t left = len - (int64_t)c * kC - 32 * ch;
+      const int nv = (int)(left < 32 ? left : 32);
+      const Rec &rc = s.rec[c % 3].r;
+      // While KS runs: the values and factors of R.
+      wait(&s.fullr[c % 3], (c / 3) & 1, 13);
+      wait(&s.fullv[par], (c >> 1) & 1, 13);
+      uint16_t v[32];
+      f2 nb[16];
       {
-        const f2 fR = mk2(pow2i(eR), pow2i(eR)), fK = mk2(-pow2i(-eS), -pow2i(-eS));
+        const uint16_t *vp = reinterpret_cast<const uint16_t *>(&s.v[par][32 * ch][cv]);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = vp[j * kV];
+        if (nv < 32) {  // rows behind the end may hold anything
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j >= nv) v[j] = 0;
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const float4 bv = *reinterpret_cast<const float4 *>(&rc.bv[32 * ch + 4 * q]);
-          const float4 bk = *reinterpret_cast<const float4 *>(&rc.bk[32 * ch + 4 * q]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t w = vv[2 * q + e];
-            x[2 * q + e] = mul2(mul2(e ? mk2(bv.z, bv.w) : mk2(bv.x, bv.y), fR), mk2(bf16lo(w), bf16hi(w)));
-            nb[2 * q + e] = mul2(mul2(e ? mk2(bk.z, bk.w) : mk2(bk.x, bk.y), fK), fR);
-          }
+          const float4 ek = *reinterpret_cast<const float4 *>(&rc.ek[32 * ch + 4 * q]);
+          nb[2 * q] = mk2(ek.x, ek.y);
+          nb[2 * q + 1] = mk2(ek.z, ek.w);
         }
       }
-      if (ch == 0 && lane == 0) {
-        s.ysc[par][quarter][0] = pow2i(-eS);
-        s.ysc[par][quarter][1] = pow2i(-eR - eT);
-      }
+      const uint32_t sv = __float_as_uint(pow2i(eS)) >> 16;  // 2^eS in bfloat16
       // R
       wait(&s.ksdone, ph, 14);
       tc_fence_after();
@@ -1067,7 +1066,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           const uint32_t a = q < 8 ? r0[2 * q] : r1[2 * q - 16], b = q < 8 ? r0[2 * q + 1] : r1[2 * q - 15];
-          split_h2(fma2(nb[q], mk2(__uint_as_float(a), __uint_as_float(b)), x[q]), hi[q], lo[q]);
+          f2 x = mul2(nb[q], mk2(__uint_as_float(a), __uint_as_float(b)));
+          x = mk2(fma_bf16(v[2 * q], (uint16_t)sv, x.x), fma_bf16(v[2 * q + 1], (uint16_t)sv, x.y));
+          split_h2(x, hi[q], lo[q]);
         }
         tmem_st16(tb + lane_base + kColR + 32 * ch, hi);
         tmem_st16(tb + lane_base + kColR + 32 * ch + 16, lo);
@@ -1076,9 +1077,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.rready);
-      // U and U'
+      // While the product with T runs: the next chunk's scale (U' takes it
+      // already, so that dS comes out in it), from a bound of its state.
+      pair_sync(quarter);
+      if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
+      const float gC = rc.gC;
+      const int eT = (int)rc.eT;
+      const float bS = fabsf(gC) * smax + 128.f * (row_sum(c) * bound_R(c, smax));
+      int eN = scale_exp(bS);
+      if (c + 1 < nch) {
+        wait(&s.conv[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
+        wait(&s.fullr[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
+        eN = scale_exp(fmaxf(bS, fmaxf(1.f, row_sum(c + 1)) * bound_R(c + 1, bS)));
+      }
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s.vfree[par]);  // (the maximum of V goes with it)
+        if (ch == 0) s.ysc[c % 3][quarter] = pow2i(-eS);
+      }
       {
-        const f2 fU = mk2(pow2i(eN - eR - eT), pow2i(eN - eR - eT));
+        const f2 fU = mk2(pow2i(eN - eS - eT), pow2i(eN - eS - eT));
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float4 cu = *reinterpret_cast<const float4 *>(&rc.cu[32 * ch + 4 * q]);
@@ -1086,6 +1104,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           nb[2 * q + 1] = mul2(mk2(cu.z, cu.w), fU);
         }
       }
+      const float un = pow2i(-eT);  // 1 but for very large T
+      // U and U'
       wait(&s.udone, ph, 15);
       tc_fence_after();
       {
@@ -1097,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 16; ++q) {
           const uint32_t a = q < 8 ? r0[2 * q] : r1[2 * q - 16], b = q < 8 ? r0[2 * q + 1] : r1[2 * q - 15];
           const f2 y = mk2(__uint_as_float(a), __uint_as_float(b));
-          uh[q] = pack_h2(y.x, y.y);
+          uh[q] = eT == 0 ? pack_h2(y.x, y.y) : pack_h2(y.x * un, y.y * un);
           split_h2(mul2(y, nb[q]), hi[q], lo[q]);
         }
         tmem_st16(tb + lane_base + kColU2 + 32 * ch, hi);
@@ -1108,8 +1128,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.uready);
-      // while dS runs: the next chunk's values
-      if (c + 1 < nch) values(c + 1);
       // the state
       wait(&s.supdone, ph, 16);
       tc_fence_after();
@@ -1126,10 +1144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            f2 &v = st[16 * i + j];
+            f2 &w = st[16 * i + j];
             const uint32_t a = r[j >> 3][2 * (j & 7)], b = r[j >> 3][2 * (j & 7) + 1];
-            v = fma2(v, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
-            split_h2(v, hi[j], lo[j]);
+            w = fma2(w, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
+            split_h2(w, hi[j], lo[j]);
             mh = maxabs_h2(mh, hi[j]);
           }
           tmem_st16(mycol + 32 * i, hi);
@@ -1164,10 +1182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 bool encode(CUtensorMap *m, const void *ptr, int64_t dim, int64_t heads, int64_t rows, int64_t row,
-            uint32_t box, CUtensorMapSwizzle sw) {
+            uint32_t box, CUtensorMapSwizzle sw, uint32_t tokens = kC) {
   const uint64_t dims[3] = {(uint64_t)dim, (uint64_t)heads, (uint64_t)rows};
   const uint64_t strides[2] = {(uint64_t)dim * 2, (uint64_t)row * 2};
-  const uint32_t b[3] = {box, 1, kC};
+  const uint32_t b[3] = {box, 1, tokens};
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, b, sw);
 }
 
@@ -1217,7 +1235,7 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   if (!encode(&mK, p.k, p.K, p.Hk, p.rows, p.k_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&mQ, p.q, p.K, p.Hk, p.rows, p.q_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&mV, p.v, p.V, p.H, p.rows, p.v_row, kV, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !encode(&mY, p.y, p.V, p.H, p.rows, p.H * p.V, 32, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !encode(&mY, p.y, p.V, p.H, p.rows, p.H * p.V, 32, CU_TENSOR_MAP_SWIZZLE_NONE, kC / 2))
     return cudaErrorInvalidValue;
   const cudaError_t e = cudaMemsetAsync(q.status, 0, sizeof(int), s);
   if (e != cudaSuccess) return e;
