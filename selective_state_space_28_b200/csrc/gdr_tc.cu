@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 //   19     copies of V ([64 x 128], two stages).
 constexpr int kThreads = 640;
 // Registers a thread of the groups; together the launch's 640 x 96.
-constexpr int kRegChain = 160, kRegSide = 64, kRegIssue = 32;
+constexpr int kRegChain = 168, kRegSide = 56, kRegIssue = 32;
 static_assert(256 * kRegChain + 256 * kRegSide + 128 * kRegIssue <= kThreads * 96, "register split");
 
 // TMEM columns.  dS lands where S's pieces are (they are rewritten from it),
@@ -632,10 +632,11 @@ template <int KD> struct __align__(1024) GdrSmem {
   uint8_t kq[3][KD / 64][128 * 128];  // [stage][slab]: rows 0-63 keys, 64-127 queries
   __nv_bfloat16 v[2][kC][kV];
   struct __align__(1024) { Rec r; } rec[3];
-  __align__(128) __nv_bfloat16 y[4][kC / 2][32];  // half a chunk's y, a warp's 32 columns
+  __align__(128) __nv_bfloat16 y[4][2][kC / 2][32];  // two halves of a chunk's y, a warp's 32 columns
   // maxima, by lane quarter (and half); of a chunk's y, the scale, and a warp's
   // factors with it
-  float vmax[2][4], smax[4][2], ysc[3][4], yfac[4][kC];
+  float smax[4][2], ysc[3][4], yfac[4][kC];
+  float4 bound[3][4];  // of a chunk, by lane quarter: see the chain
   uint64_t fullk[3], conv[3], empty[3], fullr[3], rfree[3], yfree[2], fullv[2], vfree[2], sready[2];
   uint64_t ksdone, rready, udone, uready, supdone, pudone;
   uint32_t taddr;
@@ -683,6 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int cv = 32 * quarter + lane;
   const bool live = v0 + cv < p.V;
   const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
+  const float kNorm = KD == 128 ? 11.32f : 8.f;  // sqrt(KD): |S^T k| <= |k| sqrt(KD) max |S|
 
   if (nch == 0) {  // an empty sequence hands its state on
     if (warp < 8 && p.h_last && live) {
@@ -885,8 +887,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 4; ++i) {
         uint32_t r[16], out[8];
         tmem_ld16(tb + lane_base + kColY + 64 * par + 16 * i, r);
-        if (whole && !(i & 1)) {  // the half before has left
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (whole && !(i & 1)) {  // the half two before has left
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
           __syncwarp();
         }
         tmem_ld_wait();
@@ -899,14 +901,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           out[2 * q + 1] = pack_bf16x2(o1.x, o1.y);
         }
         if (whole) {
-          uint16_t *sy = reinterpret_cast<uint16_t *>(&s.y[quarter][16 * (i & 1)][lane]);
+          uint16_t *sy = reinterpret_cast<uint16_t *>(&s.y[quarter][i >> 1][16 * (i & 1)][lane]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) sy[32 * j] = (uint16_t)(out[j / 2] >> (16 * (j & 1)));
           if (i & 1) {
             fence_async_smem();
             __syncwarp();
             if (lane == 0 && v0 + 32 * quarter < p.V) {
-              tma_store_3d(&mY, s.y[quarter], (int)v0 + 32 * quarter, (int)hd,
+              tma_store_3d(&mY, s.y[quarter][i >> 1], (int)v0 + 32 * quarter, (int)hd,
                            (int)(t0 + (int64_t)c * kC + 16 * (i - 1)));
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");
             }
@@ -932,6 +934,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int c = 0; c < nch; ++c) {
       const int64_t left = len - (int64_t)c * kC;
       const Rec &rc = s.rec[c % 3].r;
+      wait(&s.fullr[c % 3], (c / 3) & 1, 11);
+      const float f = pt < 64 ? rc.fk[tok] : rc.fq[tok];
+      const float eg = pt < 64 ? 1.f : rc.eg[tok];
+      const uint32_t f2x = __byte_perm(__float_as_uint(f), 0, 0x3232);  // (a power of two: exact)
+      wait(&s.fullk[c % 3], (c / 3) & 1, 12);
+      uint8_t *base = &s.kq[c % 3][0][0];
+      const bool on = tok < left;  // rows behind the end may hold anything
+#pragma unroll 8
+      for (int i = 0; i < NP * 8; ++i) {
+        uint4 *at = reinterpret_cast<uint4 *>(base + (i >> 3) * (128 * 128) + sw128(pt, i & 7));
+        const uint4 u = *at;
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
+          if (pt >= 64) y = mul2(y, mk2(eg, eg));
+          w[x] = on ? pack_h2(y.x, y.y) : 0u;
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_async_smem();
       {  // the largest finite value of this warp's quarter of V
         wait(&s.fullv[c & 1], (c >> 1) & 1, 18);
         const uint4 *vp = reinterpret_cast<const uint4 *>(&s.v[c & 1][lane >> 2][32 * quarter + 8 * (lane & 3)]);
@@ -954,36 +977,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         mx = warp_max(mx);
-        if (lane == 0) s.vmax[c & 1][quarter] = mx;
+        // with m the state's largest value: |R| max(1, row sum of T) <= x + y m,
+        // and the next state's <= z + w m
+        const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn * kNorm;
+        if (lane == 0)
+          s.bound[c % 3][quarter] =
+              make_float4(t1 * mx, t1 * en, 128.f * tn * mx, fmaf(128.f * tn, en, fabsf(rc.gC)));
       }
-      wait(&s.fullr[c % 3], (c / 3) & 1, 11);
-      const float f = pt < 64 ? rc.fk[tok] : rc.fq[tok];
-      const float eg = pt < 64 ? 1.f : rc.eg[tok];
-      const uint32_t f2x = __byte_perm(__float_as_uint(f), 0, 0x3232);  // (a power of two: exact)
-      wait(&s.fullk[c % 3], (c / 3) & 1, 12);
-      uint8_t *base = &s.kq[c % 3][0][0];
-      const bool on = tok < left;  // rows behind the end may hold anything
-#pragma unroll 4
-      for (int i = 0; i < NP * 8; ++i) {
-        uint4 *at = reinterpret_cast<uint4 *>(base + (i >> 3) * (128 * 128) + sw128(pt, i & 7));
-        const uint4 u = *at;
-        uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
-          if (pt >= 64) y = mul2(y, mk2(eg, eg));
-          w[x] = on ? pack_h2(y.x, y.y) : 0u;
-        }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.conv[c % 3]);
     }
   } else {
     // ------------------------------------------------------------ the chain
     reg_alloc<kRegChain>();
-    const float kNorm = KD == 128 ? 11.32f : 8.f;  // sqrt(KD): |S^T k| <= |k| sqrt(KD) max |S|
     f2 st[KH / 2];  // the half row of this lane, scaled by 2^eS
     float m = 0.f;
 #pragma unroll
@@ -999,13 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
     // One scale 2^e a chunk for S, R and U.  |R| <= max |v| + |ek k| sqrt(K)
     // max |S|, |U| <= (T's row sums) max |R|, |dS| <= sum |k| |U'| <= 128 max |U|.
-    auto bound_R = [&](int c, float smax) {
-      return s.vmax[c & 1][quarter] + s.rec[c % 3].r.ekn * kNorm * smax;
-    };
-    auto row_sum = [&](int c) { return s.rec[c % 3].r.tn * pow2i(-(int)s.rec[c % 3].r.eT); };
-    wait(&s.fullr[0], 0, 13);
     wait(&s.conv[0], 0, 13);
-    int eS = scale_exp(fmaxf(smax, fmaxf(1.f, row_sum(0)) * bound_R(0, smax)));
+    int eS = scale_exp(fmaxf(smax, fmaf(s.bound[0][quarter].y, smax, s.bound[0][quarter].x)));
     // S's pieces, hi and lo of 32 values within their own dS columns
     const uint32_t mycol = tb + lane_base + kColS + ch * KH;
     {
@@ -1033,9 +1034,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t left = len - (int64_t)c * kC - 32 * ch;
       const int nv = (int)(left < 32 ? left : 32);
       const Rec &rc = s.rec[c % 3].r;
-      // While KS runs: the values and factors of R.
-      wait(&s.fullr[c % 3], (c / 3) & 1, 13);
-      wait(&s.fullv[par], (c >> 1) & 1, 13);
+      // While KS runs: the values and factors of R, and the next chunk's scale
+      // (U' takes it already, so that dS comes out in it) from a bound of its
+      // state.  (A chunk that is converted has its V and record.)
+      const bool more = c + 1 < nch;
+      if (more) wait(&s.conv[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
+      const float4 bn = s.bound[c % 3][quarter], bx = s.bound[more ? (c + 1) % 3 : c % 3][quarter];
+      const float gC = rc.gC;
+      const int eT = (int)rc.eT;
       uint16_t v[32];
       f2 nb[16];
       {
@@ -1055,6 +1061,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const uint32_t sv = __float_as_uint(pow2i(eS)) >> 16;  // 2^eS in bfloat16
+      pair_sync(quarter);
+      if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
+      const float bS = fmaf(bn.w, smax, bn.z);
+      const int eN = scale_exp(more ? fmaxf(bS, fmaf(bx.y, bS, bx.x)) : bS);
+      if (lane == 0) {
+        mbar_arrive(&s.vfree[par]);
+        if (ch == 0) s.ysc[c % 3][quarter] = pow2i(-eS);
+      }
       // R
       wait(&s.ksdone, ph, 14);
       tc_fence_after();
@@ -1077,24 +1091,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.rready);
-      // While the product with T runs: the next chunk's scale (U' takes it
-      // already, so that dS comes out in it), from a bound of its state.
-      pair_sync(quarter);
-      if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
-      const float gC = rc.gC;
-      const int eT = (int)rc.eT;
-      const float bS = fabsf(gC) * smax + 128.f * (row_sum(c) * bound_R(c, smax));
-      int eN = scale_exp(bS);
-      if (c + 1 < nch) {
-        wait(&s.conv[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
-        wait(&s.fullr[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
-        eN = scale_exp(fmaxf(bS, fmaxf(1.f, row_sum(c + 1)) * bound_R(c + 1, bS)));
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.vfree[par]);  // (the maximum of V goes with it)
-        if (ch == 0) s.ysc[c % 3][quarter] = pow2i(-eS);
-      }
       {
         const f2 fU = mk2(pow2i(eN - eS - eT), pow2i(eN - eS - eT));
 #pragma unroll
@@ -1136,16 +1132,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const f2 g2 = mk2(gn, gn);
         eS = eN;
         uint32_t mh = 0u;
+        uint32_t r[KH / 32][2][16];
 #pragma unroll
         for (int i = 0; i < KH / 32; ++i) {
-          uint32_t r[2][16], hi[16], lo[16];
-          tmem_ld16(mycol + 32 * i, r[0]);
-          tmem_ld16(mycol + 32 * i + 16, r[1]);
-          tmem_ld_wait();
+          tmem_ld16(mycol + 32 * i, r[i][0]);
+          tmem_ld16(mycol + 32 * i + 16, r[i][1]);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < KH / 32; ++i) {
+          uint32_t hi[16], lo[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             f2 &w = st[16 * i + j];
-            const uint32_t a = r[j >> 3][2 * (j & 7)], b = r[j >> 3][2 * (j & 7) + 1];
+            const uint32_t a = r[i][j >> 3][2 * (j & 7)], b = r[i][j >> 3][2 * (j & 7) + 1];
             w = fma2(w, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
             split_h2(w, hi[j], lo[j]);
             mh = maxabs_h2(mh, hi[j]);
