@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     const bool in = on && (isk ? j < tok : j <= tok);
     dec[q] = in ? rowf * s.f[j] * ex2(d.x + d.y) : 0.f;
   }
-#pragma unroll
+#pragma unroll 1
   for (int J = 0; J < 4; ++J) {
     float x[16];
     if ((J >> 1) <= blk) {
@@ -1028,47 +1028,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(&s.sready[ch]);
 
-    for (int c = 0; c < nch; ++c) {
-      const int par = c & 1;
-      const uint32_t ph = par;
+    // The values of a chunk that is converted (and so has its V and record), two
+    // tokens a register.
+    uint32_t vv[16];
+    auto values = [&](int c) {
       const int64_t left = len - (int64_t)c * kC - 32 * ch;
-      const int nv = (int)(left < 32 ? left : 32);
+      const uint16_t *vp = reinterpret_cast<const uint16_t *>(&s.v[c & 1][32 * ch][cv]);
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        vv[q] = (uint32_t)vp[2 * q * kV] | ((uint32_t)vp[(2 * q + 1) * kV] << 16);
+      if (left < 32) {  // rows behind the end may hold anything
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          if (2 * q >= left) vv[q] = 0u;
+          else if (2 * q + 1 >= left) vv[q] &= 0xffffu;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.vfree[c & 1]);
+    };
+    values(0);
+    for (int c = 0; c < nch; ++c) {
+      const uint32_t ph = c & 1;
       const Rec &rc = s.rec[c % 3].r;
-      // While KS runs: the values and factors of R, and the next chunk's scale
-      // (U' takes it already, so that dS comes out in it) from a bound of its
-      // state.  (A chunk that is converted has its V and record.)
+      // While KS runs: the factors of R, and the next chunk's scale (U' takes it
+      // already, so that dS comes out in it) from a bound of its state.
       const bool more = c + 1 < nch;
+      f2 nb[16];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 ek = *reinterpret_cast<const float4 *>(&rc.ek[32 * ch + 4 * q]);
+        nb[2 * q] = mk2(ek.x, ek.y);
+        nb[2 * q + 1] = mk2(ek.z, ek.w);
+      }
       if (more) wait(&s.conv[(c + 1) % 3], ((c + 1) / 3) & 1, 17);
       const float4 bn = s.bound[c % 3][quarter], bx = s.bound[more ? (c + 1) % 3 : c % 3][quarter];
       const float gC = rc.gC;
       const int eT = (int)rc.eT;
-      uint16_t v[32];
-      f2 nb[16];
-      {
-        const uint16_t *vp = reinterpret_cast<const uint16_t *>(&s.v[par][32 * ch][cv]);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = vp[j * kV];
-        if (nv < 32) {  // rows behind the end may hold anything
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j >= nv) v[j] = 0;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 ek = *reinterpret_cast<const float4 *>(&rc.ek[32 * ch + 4 * q]);
-          nb[2 * q] = mk2(ek.x, ek.y);
-          nb[2 * q + 1] = mk2(ek.z, ek.w);
-        }
-      }
-      const uint32_t sv = __float_as_uint(pow2i(eS)) >> 16;  // 2^eS in bfloat16
+      const uint32_t sv = __byte_perm(__float_as_uint(pow2i(eS)), 0, 0x3232);  // 2^eS in bfloat16, twice
       pair_sync(quarter);
       if (c > 0) smax = pow2i(-eS) * fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
       const float bS = fmaf(bn.w, smax, bn.z);
       const int eN = scale_exp(more ? fmaxf(bS, fmaf(bx.y, bS, bx.x)) : bS);
-      if (lane == 0) {
-        mbar_arrive(&s.vfree[par]);
-        if (ch == 0) s.ysc[c % 3][quarter] = pow2i(-eS);
-      }
+      if (ch == 0 && lane == 0) s.ysc[c % 3][quarter] = pow2i(-eS);
       // R
       wait(&s.ksdone, ph, 14);
       tc_fence_after();
@@ -1081,8 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 16; ++q) {
           const uint32_t a = q < 8 ? r0[2 * q] : r1[2 * q - 16], b = q < 8 ? r0[2 * q + 1] : r1[2 * q - 15];
           f2 x = mul2(nb[q], mk2(__uint_as_float(a), __uint_as_float(b)));
-          x = mk2(fma_bf16(v[2 * q], (uint16_t)sv, x.x), fma_bf16(v[2 * q + 1], (uint16_t)sv, x.y));
-          split_h2(x, hi[q], lo[q]);
+          split_h2(fma_bf16x2(vv[q], sv, x), hi[q], lo[q]);
         }
         tmem_st16(tb + lane_base + kColR + 32 * ch, hi);
         tmem_st16(tb + lane_base + kColR + 32 * ch + 16, lo);
@@ -1124,6 +1125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.uready);
+      // While dS runs: the next chunk's values.
+      if (more) values(c + 1);
       // the state
       wait(&s.supdone, ph, 16);
       tc_fence_after();
@@ -1132,20 +1135,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const f2 g2 = mk2(gn, gn);
         eS = eN;
         uint32_t mh = 0u;
-        uint32_t r[KH / 32][2][16];
 #pragma unroll
         for (int i = 0; i < KH / 32; ++i) {
-          tmem_ld16(mycol + 32 * i, r[i][0]);
-          tmem_ld16(mycol + 32 * i + 16, r[i][1]);
-        }
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < KH / 32; ++i) {
+          uint32_t r[2][16];
+          tmem_ld16(mycol + 32 * i, r[0]);
+          tmem_ld16(mycol + 32 * i + 16, r[1]);
+          tmem_ld_wait();
           uint32_t hi[16], lo[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             f2 &w = st[16 * i + j];
-            const uint32_t a = r[i][j >> 3][2 * (j & 7)], b = r[i][j >> 3][2 * (j & 7) + 1];
+            const uint32_t a = r[j >> 3][2 * (j & 7)], b = r[j >> 3][2 * (j & 7) + 1];
             w = fma2(w, g2, mk2(__uint_as_float(a), __uint_as_float(b)));
             split_h2(w, hi[j], lo[j]);
             mh = maxabs_h2(mh, hi[j]);
