@@ -67,18 +67,22 @@ struct Rec {
   uint8_t T[2][kC * 128];  // hi, lo: 64 x 64 float16, 128-byte swizzled rows
   uint8_t P[kC * 128];
   float ek[kC], cu[kC], cq[kC];  // factors of KS (negative), U' and y
-  float fk[kC], fq[kC], eg[kC];  // of keys and queries: powers of two; decays of queries
+  float fq[kC];                  // of queries: powers of two and decays
   float gC, ekn, tn, eT;         // e^g_63; bounds of ek |k| and of T's rows (scaled); T's exponent
   float pad[12];
 };
+// and, for a chunk and key head, the keys as scaled float16: KD / 64 slabs of
+// 64 x 64, 128-byte swizzled rows.
+constexpr size_t kSlab = kC * 128;
 constexpr size_t kRecT = 2 * kC * 128;
-static_assert(sizeof(Rec) == 26176 && sizeof(Rec) % 16 == 0, "a record is copied in 16-byte units");
+static_assert(sizeof(Rec) == 25664 && sizeof(Rec) % 16 == 0, "a record is copied in 16-byte units");
 
 struct GdrTcParams {
   GdrParams p;
   int64_t vtiles;
   int64_t chunks;  // of a sequence (dense), or 0: packed
-  uint8_t *rec;
+  uint8_t *rec;   // [slot][head]
+  uint8_t *keys;  // [slot][key head][slab]
   int *status;
 };
 
@@ -161,11 +165,6 @@ __device__ __forceinline__ uint32_t maxabs_bf2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-__device__ __forceinline__ float fma_bf16(uint16_t x, uint16_t y, float c) {
-  float d;
-  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(x), "h"(y), "f"(c));
-  return d;
 }
 // Two bfloat16 times a bfloat16, plus c, in float32.
 __device__ __forceinline__ f2 fma_bf16x2(uint32_t x, uint32_t y, f2 c) {
@@ -437,17 +436,33 @@ __global__ void __launch_bounds__(kPrepThreads)
     s.bv[tok] = nf * b;
     fac[0 * kC + tok] = -nf * eg;                              // ek
     fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
-    fac[3 * kC + tok] = f;                                     // fk
     s.f[tok] = f;
     s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
     const float m = warp_max(2.f * nf * eg);
     if (lane == 0) s.ekn[pw] = m;
   } else {
     fac[2 * kC + tok] = p.scale * nf;  // cq
-    fac[4 * kC + tok] = f;             // fq
-    fac[5 * kC + tok] = eg;
+    fac[3 * kC + tok] = f * eg;        // fq
   }
   __syncthreads();  // f, h
+  if (hd % (p.H / p.Hk) == 0) {  // the keys, scaled; rows behind the end may hold anything
+    uint8_t *out = tp.keys + (rs * p.Hk + g) * (int64_t)(NP * kSlab);
+#pragma unroll
+    for (int i = 0; i < NP * 4; ++i) {
+      const int at = (i & 3) * kPrepThreads + pt;  // 16 bytes of the slab: any swizzle
+      const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[i >> 2][16 * at]);
+      const float fr = s.f[at >> 3];
+      const uint32_t f2x = __byte_perm(__float_as_uint(fr), 0, 0x3232);  // (a power of two: exact)
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f2 y = fma_bf16x2(w[e], f2x, mk2(0.f, 0.f));
+        w[e] = (at >> 3) < nv ? pack_h2(y.x, y.y) : 0u;
+      }
+      *reinterpret_cast<uint4 *>(out + (i >> 2) * kSlab + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncthreads();  // A and P take the keys' place
+  }
 
   // A and P, 16 columns at a time.  In the row's own 16-token block the decays
   // are taken element by element; in blocks before it they go by way of the
@@ -587,10 +602,10 @@ __global__ void __launch_bounds__(kPrepThreads)
     *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
   }
   if (pw == 3 && lane == 0) {
-    fac[6 * kC] = gtot;
-    fac[6 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
-    fac[6 * kC + 2] = tn * sc.x;
-    fac[6 * kC + 3] = (float)eT;
+    fac[4 * kC] = gtot;
+    fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
+    fac[4 * kC + 2] = tn * sc.x;
+    fac[4 * kC + 3] = (float)eT;
   }
   fence_async_smem();
   if (!ok && tp.status) atomicExch(tp.status, 1);
@@ -612,9 +627,11 @@ __global__ void __launch_bounds__(kPrepThreads)
 //   0-7    the chain: two warps per lane quarter, each with half of the columns
 //          (tokens of R and U, key dimensions of S): R from KS and V; U' from
 //          the product with T; the state from dS.
-//   8-11   keys and queries to scaled float16, in place, a chunk ahead.
+//   8-11   queries to scaled float16, in place, and the chunk's bounds, a chunk
+//          ahead.
 //   12-15  y from QS and PU, a chunk behind.
-//   16     copies of K and Q ([64 x 64] slabs, 128-byte swizzle, three stages).
+//   16     copies of the scaled keys and of Q ([64 x 64] slabs, 128-byte swizzle,
+//          three stages).
 //   17     MMA issuer.
 //   18     copies of the records (three stages).
 //   19     copies of V ([64 x 128], two stages).
@@ -659,7 +676,7 @@ struct Waiter {
 
 template <int KD>
 __global__ void __launch_bounds__(kThreads, 1)
-    gdr_tc_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mQ,
+    gdr_tc_kernel(const __grid_constant__ CUtensorMap mQ,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mY,
                   const GdrTcParams tp) {
   constexpr int NP = KD / 64;        // slabs
@@ -732,8 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     reg_dealloc<kRegIssue>();
     if (warp == 16 && lane == 0) {
       // ---------------------------------------------------------- keys and queries
-      tma_prefetch_desc(&mK);
       tma_prefetch_desc(&mQ);
+      const uint8_t *keys = tp.keys + (first_slot(tp, seq, t0) * p.Hk + g) * (int64_t)(NP * kSlab);
+      pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
         const int k3 = c % 3, t = (int)(t0 + (int64_t)c * kC);
@@ -741,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_expect_tx(&s.fullk[k3], NP * 128 * 128);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-          tma_load_3d(s.kq[k3][n], &mK, &s.fullk[k3], 64 * n, (int)g, t);
+          bulk_load(s.kq[k3][n], keys + (c * p.Hk * NP + n) * (int64_t)kSlab, kSlab, &s.fullk[k3]);
           tma_load_3d(s.kq[k3][n] + kC * 128, &mQ, &s.fullk[k3], 64 * n, (int)g, t);
         }
       }
@@ -799,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t th = smem_desc(smem_u32(s.rec[c % 3].r.T[0]), 16, 1024, kSwizzle128B);
         const uint64_t tl = smem_desc(smem_u32(s.rec[c % 3].r.T[1]), 16, 1024, kSwizzle128B);
         const uint64_t dp = smem_desc(smem_u32(s.rec[c % 3].r.P), 16, 1024, kSwizzle128B);
+        wait(&s.fullk[c % 3], (c / 3) & 1, 3);
         wait(&s.conv[c % 3], (c / 3) & 1, 3);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // a half of the state at a time
@@ -930,29 +949,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8) {
     // ------------------------------------------------------------ conversion
     reg_dealloc<kRegSide>();
-    const int pt = tid - 256, tok = pt & 63;
+    const int tok = (tid - 256) >> 1, hf = tid & 1;  // two threads a query
     for (int c = 0; c < nch; ++c) {
       const int64_t left = len - (int64_t)c * kC;
       const Rec &rc = s.rec[c % 3].r;
       wait(&s.fullr[c % 3], (c / 3) & 1, 11);
-      const float f = pt < 64 ? rc.fk[tok] : rc.fq[tok];
-      const float eg = pt < 64 ? 1.f : rc.eg[tok];
-      const uint32_t f2x = __byte_perm(__float_as_uint(f), 0, 0x3232);  // (a power of two: exact)
+      const float f = rc.fq[tok];
       wait(&s.fullk[c % 3], (c / 3) & 1, 12);
-      uint8_t *base = &s.kq[c % 3][0][0];
       const bool on = tok < left;  // rows behind the end may hold anything
-#pragma unroll 8
-      for (int i = 0; i < NP * 8; ++i) {
-        uint4 *at = reinterpret_cast<uint4 *>(base + (i >> 3) * (128 * 128) + sw128(pt, i & 7));
-        const uint4 u = *at;
+#pragma unroll
+      for (int i = 0; i < NP * 4; ++i) {
+        // (the halves' accesses lie in different banks)
+        const int at = NP == 2 ? (i ^ (4 * hf)) : i + 4 * hf;
+        uint4 *qp = reinterpret_cast<uint4 *>(&s.kq[c % 3][NP == 2 ? hf : 0][0] + sw128(kC + tok, at));
+        const uint4 u = *qp;
         uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          f2 y = fma_bf16x2(w[x], f2x, mk2(0.f, 0.f));
-          if (pt >= 64) y = mul2(y, mk2(eg, eg));
+          const f2 y = mul2(mk2(bf16lo(w[x]), bf16hi(w[x])), mk2(f, f));
           w[x] = on ? pack_h2(y.x, y.y) : 0u;
         }
-        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        *qp = make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_async_smem();
       {  // the largest finite value of this warp's quarter of V
@@ -1208,7 +1225,7 @@ cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMa
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(gdr_tc_kernel<KD>, dim3((unsigned)(q.p.nseq * q.p.H * q.vtiles)),
-                          dim3(kThreads), smem, s, mK, mQ, mV, mY, q);
+                          dim3(kThreads), smem, s, mQ, mV, mY, q);
 }
 
 }  // namespace
@@ -1221,7 +1238,8 @@ bool gdr_tc_supported(const GdrParams &p) {
 }
 
 size_t gdr_tc_workspace(const GdrParams &p) {
-  return kGdrStatusBytes + (size_t)(slots_of(p) * p.H) * sizeof(Rec);
+  return kGdrStatusBytes + (size_t)(slots_of(p) * p.H) * sizeof(Rec) +
+         (size_t)(slots_of(p) * p.Hk) * (p.K <= 64 ? 1 : 2) * kSlab;
 }
 
 cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
@@ -1230,6 +1248,7 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   q.vtiles = (p.V + kV - 1) / kV;
   q.chunks = p.cu ? 0 : (p.L + kC - 1) / kC;
   q.rec = static_cast<uint8_t *>(workspace) + kGdrStatusBytes;
+  q.keys = q.rec + (size_t)(slots_of(p) * p.H) * sizeof(Rec);
   q.status = static_cast<int *>(workspace);
   CUtensorMap mK, mQ, mV, mY;
   if (!encode(&mK, p.k, p.K, p.Hk, p.rows, p.k_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
