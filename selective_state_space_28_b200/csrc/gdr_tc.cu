@@ -230,20 +230,22 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // out [16 MT x 8] = a [16 MT x 8 KT] b [8 KT x 8], rows of kAm floats.
-template <int MT, int KT>
-__device__ __forceinline__ void small_product(const float *a, const float *b, float (&out)[MT][4]) {
+// k starts at step k0 (b holds zeros before it); LOWER: a is lower triangular.
+template <int MT, int KT, bool LOWER>
+__device__ __forceinline__ void small_product(const float *a, const float *b, int k0, float (&out)[MT][4]) {
   const int lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[m][e] = 0.f;
 #pragma unroll 1  // (short code: several CTAs share the instruction cache)
-  for (int k = 0; k < KT; ++k) {
+  for (int k = k0; k < KT; ++k) {
     uint32_t bh[2], bl[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) split_tf32(b[(8 * k + t + 4 * e) * kAm + r], bh[e], bl[e]);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
+      if (LOWER && k >= 2 * m + 2) continue;
       uint32_t ah[4], al[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -307,16 +309,6 @@ __global__ void __launch_bounds__(kPrepThreads)
     mbar_init(&s.full, 1);
     mbar_init(&s.done, 1);
     fence_mbar_init();
-  }
-  if (pw == 0) {
-    tmem_alloc(&s.taddr, 64);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = s.taddr;
-  if (pt == 0) {
     mbar_expect_tx(&s.full, NP * 128 * 128);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
@@ -325,42 +317,59 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
   }
   __syncwarp();
-  float gtot = 1.f;
+  if (pw == 1) {
+    tmem_alloc(&s.taddr, 64);
+    tmem_relinquish();
+  }
+  int64_t g63x = 0;
   if (pw == 3) {  // the gates: lane l has tokens 2 l and 2 l + 1
-    double gs[2];
-    float be[2];
+    float dtv[2] = {}, be[2] = {};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (2 * lane + e < nv) {
+        const int64_t at = t0 + 2 * lane + e;
+        if (p.dt) dtv[e] = ld(static_cast<const __nv_bfloat16 *>(p.dt) + at * p.dt_row + hd);
+        be[e] = ld(static_cast<const __nv_bfloat16 *>(p.beta) + at * p.beta_row + hd);
+      }
+    }
     const float Ah = p.dt ? p.A[hd] : 0.f;
     const float bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
+    // log2 of the decays summed in fixed point, 2^-44 a unit: exact, and the
+    // sums of 64 fit (each at least -256: zero either way)
+    int64_t gs[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float l2 = 0.f, b = 0.f;
       if (2 * lane + e < nv) {
-        const int64_t row = t0 + 2 * lane + e;
         if (p.dt) {
-          float d = ld(static_cast<const __nv_bfloat16 *>(p.dt) + row * p.dt_row + hd) + bias;
+          float d = dtv[e] + bias;
           if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
-          l2 = d * Ah * kLog2e;
-          if (l2 < -256.f) l2 = -256.f;  // zero either way; keeps the sums exact
+          l2 = fmaxf(d * Ah * kLog2e, -256.f);
         }
-        b = gdr_beta<__nv_bfloat16>(p, row, hd);
+        b = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be[e] * kLog2e)) : be[e];
       }
-      gs[e] = (double)l2;
-      be[e] = b;
+      gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
+      s.beta[2 * lane + e] = b;
     }
-    double sum = gs[0] + gs[1];
+    int64_t sum = gs[0] + gs[1];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const double o = __shfl_up_sync(0xffffffffu, sum, off);
+      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
       if (lane >= off) sum += o;
     }
-    const double g1 = sum, g0 = sum - gs[1];
-    s.g[2 * lane] = mk2((float)g0, (float)(g0 - (double)(float)g0));
-    s.g[2 * lane + 1] = mk2((float)g1, (float)(g1 - (double)(float)g1));
-    s.beta[2 * lane] = be[0];
-    s.beta[2 * lane + 1] = be[1];
-    // the chunk's decay multiplies the state once a chunk: exact
-    gtot = (float)exp2(__shfl_sync(0xffffffffu, g1, 31));
+    g63x = __shfl_sync(0xffffffffu, sum, 31);
+    // hi: multiples of 2^-10 (24 bits); lo: the rest below, in 2^-34
+    auto parts = [](int64_t g) {
+      return mk2((float)(int)(g >> 34) * 0.0009765625f,
+                 (float)(int)((g & ((1ll << 34) - 1)) >> 10) * 5.8207660913467407e-11f);
+    };
+    s.g[2 * lane] = parts(sum - gs[1]);
+    s.g[2 * lane + 1] = parts(sum);
   }
+  tc_fence_before();
+  __syncthreads();  // the barriers, TMEM's address, the gates
+  tc_fence_after();
+  const uint32_t tb = s.taddr;
   bool ok = mbar_wait(&s.full, 0, kWaitLimit);
   if (pw == 0) {
     if (elect_one()) {
@@ -391,23 +400,33 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
   ok = mbar_wait(&s.done, 0, kWaitLimit) && ok;
   tc_fence_after();
-  __syncthreads();  // the gates and |q|^2; every thread is done with the rows
+  __syncthreads();  // |q|^2; every thread is done with the rows
 
   const int tok = pt & 63;
   const bool isk = pt < 64, on = tok < nv;
   const uint32_t grow = tb + ((uint32_t)(32 * pw) << 16);
+  // of G this row's columns of its own 32-token block; own: of its 16-token block
+  const int blk = pw & 1;
+  const bool up = lane >= 16;  // the second of the two 16-token blocks
+  uint32_t r0[16], own[16];
+  {
+    uint32_t r1[16];
+    tmem_ld16(grow + 32 * blk, r0);
+    tmem_ld16(grow + 32 * blk + 16, r1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) own[q] = up ? r1[q] : r0[q];
+  }
   float n2;
   if (isk) {
-    n2 = 0.f;
-    uint32_t r[16];
+    uint32_t t[8];  // own[lane & 15], bit by bit of the index
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      tmem_ld16(grow + 32 * pw + 16 * i, r);
-      tmem_ld_wait();
+    for (int q = 0; q < 8; ++q) t[q] = lane & 8 ? own[q + 8] : own[q];
 #pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (lane == 16 * i + q) n2 = __uint_as_float(r[q]);
-    }
+    for (int q = 0; q < 4; ++q) t[q] = lane & 4 ? t[q + 4] : t[q];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) t[q] = lane & 2 ? t[q + 2] : t[q];
+    n2 = __uint_as_float(lane & 1 ? t[1] : t[0]);
   } else {
     n2 = s.qq[tok];
   }
@@ -469,54 +488,74 @@ __global__ void __launch_bounds__(kPrepThreads)
   // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
   // above 1.
   uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
-  const int blk = pw & 1, own = tok >> 4;
-  float dec[16];
+  const bool part = nv < kC;
+  auto put = [&](int J, const f2(&x)[8]) {
+    f2 z[8];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const int j = 16 * own + q;
-    const f2 gj = s.g[j];
-    const f2 d = add2(gi, mk2(-gj.x, -gj.y));
-    const bool in = on && (isk ? j < tok : j <= tok);
-    dec[q] = in ? rowf * s.f[j] * ex2(d.x + d.y) : 0.f;
-  }
-#pragma unroll 1
-  for (int J = 0; J < 4; ++J) {
-    float x[16];
-    if ((J >> 1) <= blk) {
-      uint32_t r[16];
-      tmem_ld16(grow + 16 * J, r);
-      const f2 ge = s.g[16 * J + 15];
-      const float fr = on && J < own ? rowf * ex2((gi.x - ge.x) + (gi.y - ge.y)) : 0.f;
-      float w[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        w[q] = fr * s.h[16 * J + q];
-        if (J == own) w[q] = dec[q];
-      }
-      tmem_ld_wait();
-      // (a product that is left out may be anything, NaN included)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = w[q] != 0.f ? __uint_as_float(r[q]) * w[q] : 0.f;
-    } else {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) x[q] = 0.f;
-    }
+    for (int q = 0; q < 8; ++q) z[q] = part && !on ? mk2(0.f, 0.f) : x[q];  // (may hold anything)
     if (isk) {
-      if ((J >> 1) <= blk) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
-              make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-      }
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
+            make_float4(z[2 * q].x, z[2 * q].y, z[2 * q + 1].x, z[2 * q + 1].y);
     } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
         *reinterpret_cast<uint4 *>(P + sw128(tok, 2 * J + q)) =
-            make_uint4(pack_h2(x[8 * q], x[8 * q + 1]), pack_h2(x[8 * q + 2], x[8 * q + 3]),
-                       pack_h2(x[8 * q + 4], x[8 * q + 5]), pack_h2(x[8 * q + 6], x[8 * q + 7]));
+            make_uint4(pack_h2(z[4 * q].x, z[4 * q].y), pack_h2(z[4 * q + 1].x, z[4 * q + 1].y),
+                       pack_h2(z[4 * q + 2].x, z[4 * q + 2].y), pack_h2(z[4 * q + 3].x, z[4 * q + 3].y));
+    }
+  };
+  auto before = [&](int J, const uint32_t(&r)[16], f2(&x)[8]) {  // a block before the row's own
+    const f2 ge = s.g[16 * J + 15];
+    const float fr = rowf * ex2((gi.x - ge.x) + (gi.y - ge.y));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 h = *reinterpret_cast<const float4 *>(&s.h[16 * J + 4 * q]);
+      x[2 * q] = mul2(mul2(mk2(h.x, h.y), mk2(fr, fr)),
+                      mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])));
+      x[2 * q + 1] = mul2(mul2(mk2(h.z, h.w), mk2(fr, fr)),
+                          mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+    }
+  };
+  {
+    f2 x[8];
+    float o[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int j = (tok & ~15) + q;
+      const f2 gj = s.g[j];
+      const f2 d = add2(gi, mk2(-gj.x, -gj.y));
+      const bool in = isk ? j < tok : j <= tok;
+      o[q] = in ? __uint_as_float(own[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
+    }
+    before(2 * blk, r0, x);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = up ? x[q] : mk2(o[2 * q], o[2 * q + 1]);
+    put(2 * blk, x);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = up ? mk2(o[2 * q], o[2 * q + 1]) : mk2(0.f, 0.f);
+    put(2 * blk + 1, x);
+  }
+#pragma unroll 1
+  for (int J = 0; J < 2; ++J) {
+    f2 x[8];
+    if (blk) {
+      tmem_ld16(grow + 16 * J, r0);
+      tmem_ld_wait();
+      before(J, r0, x);
+      put(J, x);
+    } else if (!isk) {  // above P's diagonal blocks
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = mk2(0.f, 0.f);
+      put(2 + J, x);
     }
   }
   tc_fence_before();
+  // the chunk's decay multiplies the state once a chunk: exact (while the other
+  // warps invert)
+  double gtot = 0.;
+  if (pw == 3) gtot = exp2((double)g63x * 0x1p-44);
   if (isk) {
     // the inverses of this warp's two diagonal blocks, a column a lane
     __syncwarp();
@@ -550,10 +589,10 @@ __global__ void __launch_bounds__(kPrepThreads)
     const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
     float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
     float c1[1][4], c2[1][4];
-    small_product<1, 2>(&s.Am[o + 16][o], &s.Am[o][o + n], c1);
+    small_product<1, 2, false>(&s.Am[o + 16][o], &s.Am[o][o + n], pw & 1, c1);
     put_product<1>(scratch, c1, 1.f);
     __syncwarp();
-    small_product<1, 2>(&s.Am[o + 16][o + 16], scratch, c2);
+    small_product<1, 2, true>(&s.Am[o + 16][o + 16], scratch, 0, c2);
     __syncthreads();  // A21 has been read
     put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
   }
@@ -561,10 +600,10 @@ __global__ void __launch_bounds__(kPrepThreads)
   {  // and of 32: eight columns a warp
     float *scratch = &s.Am[0][32 + 8 * pw];
     float c1[2][4], c2[2][4];
-    small_product<2, 4>(&s.Am[32][0], &s.Am[0][8 * pw], c1);
+    small_product<2, 4, false>(&s.Am[32][0], &s.Am[0][8 * pw], pw, c1);
     put_product<2>(scratch, c1, 1.f);
     __syncwarp();
-    small_product<2, 4>(&s.Am[32][32], scratch, c2);
+    small_product<2, 4, true>(&s.Am[32][32], scratch, 0, c2);
     __syncthreads();
     put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
   }
@@ -602,7 +641,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
   }
   if (pw == 3 && lane == 0) {
-    fac[4 * kC] = gtot;
+    fac[4 * kC] = (float)gtot;
     fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
     fac[4 * kC + 2] = tn * sc.x;
     fac[4 * kC + 3] = (float)eT;
@@ -612,7 +651,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (pw == 0) tmem_dealloc(tb, 64);
+  if (pw == 1) tmem_dealloc(tb, 64);
   if (pt == 0) {
     uint8_t *out = tp.rec + (rs * p.H + hd) * (int64_t)sizeof(Rec);
     bulk_store(out, s.T, kRecT);
@@ -660,17 +699,18 @@ template <int KD> struct __align__(1024) GdrSmem {
 };
 static_assert(sizeof(GdrSmem<128>) + 1024 <= 232448, "GdrSmem exceeds the shared memory of a CTA");
 
-// A warp's wait: every lane polls (bounded), then the warp votes.  After one
-// that ran out the warp goes on without waiting, so that barriers stay matched.
+// A warp's wait (bounded).  After one that ran out the warp goes on without
+// waiting, so that barriers stay matched.
 struct Waiter {
   int *status;
   bool dead;
   __device__ __forceinline__ void operator()(uint64_t *bar, uint32_t parity, int code) {
     if (dead) return;
-    if (__any_sync(0xffffffffu, !mbar_wait(bar, parity, kWaitLimit))) {
-      dead = true;
-      if (status && (threadIdx.x & 31) == 0) atomicExch(status, code);
-    }
+    if (__any_sync(0xffffffffu, !mbar_wait(bar, parity, kWaitLimit))) expired(code);
+  }
+  __device__ __forceinline__ void expired(int code) {
+    dead = true;
+    if (status && (threadIdx.x & 31) == 0) atomicExch(status, code);
   }
 };
 
@@ -817,8 +857,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t th = smem_desc(smem_u32(s.rec[c % 3].r.T[0]), 16, 1024, kSwizzle128B);
         const uint64_t tl = smem_desc(smem_u32(s.rec[c % 3].r.T[1]), 16, 1024, kSwizzle128B);
         const uint64_t dp = smem_desc(smem_u32(s.rec[c % 3].r.P), 16, 1024, kSwizzle128B);
-        wait(&s.fullk[c % 3], (c / 3) & 1, 3);
-        wait(&s.conv[c % 3], (c / 3) & 1, 3);
+        auto ready = [&](int i) {  // keys, queries and record of chunk i
+          wait(&s.fullk[i % 3], (i / 3) & 1, 3);
+          wait(&s.fullr[i % 3], (i / 3) & 1, 3);
+          wait(&s.conv[i % 3], (i / 3) & 1, 3);
+        };
+        if (c == 0) ready(0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // a half of the state at a time
           wait(&s.sready[h], ph, 4);
@@ -835,7 +879,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (wait.dead) break;
         commit(&s.ksdone, ph);
-        wait(&s.fullr[c % 3], (c / 3) & 1, 6);
+        // y of the chunk two before has been read
+        if (c > 1) wait(&s.yfree[ph], ((c >> 1) - 1) & 1, 5);
         wait(&s.rready, ph, 7);
         if (wait.dead) break;
         tc_fence_after();
@@ -848,16 +893,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (x == 2 ? tl : th) + 2 * kk, id64, x + kk > 0);
         }
         commit(&s.udone, ph);
-        // y of the chunk two before has been read
-        if (c > 1) wait(&s.yfree[ph], ((c >> 1) - 1) & 1, 5);
-        if (wait.dead) break;
-        tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < KS16; ++kk)
             mma_ts(ycol, tb + kColS + rcol(kk), dq + koff(kk), id64, kk > 0);
         }
         __syncwarp();
+        if (c + 1 < nch) ready(c + 1);
         wait(&s.uready, ph, 8);
         if (wait.dead) break;
         tc_fence_after();
