@@ -81,6 +81,7 @@ struct GdrTcParams {
   GdrParams p;
   int64_t vtiles;
   int64_t chunks;  // of a sequence (dense), or 0: packed
+  int64_t units;   // records
   uint8_t *rec;   // [slot][head]
   uint8_t *keys;  // [slot][key head][slab]
   int *status;
@@ -238,7 +239,7 @@ __device__ __forceinline__ void small_product(const float *a, const float *b, in
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[m][e] = 0.f;
-#pragma unroll 1  // (short code: several CTAs share the instruction cache)
+#pragma unroll 2
   for (int k = k0; k < KT; ++k) {
     uint32_t bh[2], bl[2];
 #pragma unroll
@@ -267,14 +268,15 @@ __device__ __forceinline__ void put_product(float *o, const float (&c)[MT][4], f
           make_float2(sign * c[m][2 * e], sign * c[m][2 * e + 1]);
 }
 
-// One CTA of 128 threads per (chunk, value head).  Row pt of [K; Q] [K]^T is
+// CTAs of 128 threads, six to an SM, each over (chunk, value head) units (a
+// launch of one CTA a unit left a third of the slots empty).  Row pt of [K; Q] [K]^T is
 // thread pt's (TMEM lane pt): keys' rows make A, queries' P.  The inverse goes
 // by blocks: the four 16 x 16 diagonal blocks by forward substitution, a column
 // a lane; then twice -T22 A21 T11 for the block below two of them, the products
 // as float32 on mma (a multiply-add version read its operands from shared memory
 // four times as often, which bound the kernel: 4200 cycles a unit of SM time).
 template <int KD>
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 6)
     gdr_prep_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mQ,
                     const GdrTcParams tp) {
   constexpr int NP = KD / 64;
@@ -283,382 +285,392 @@ __global__ void __launch_bounds__(kPrepThreads)
   Smem &s = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const GdrParams &p = tp.p;
   const int pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
-  const int64_t hd = blockIdx.x % p.H, rs = blockIdx.x / p.H;
   pdl_launch_dependents();
-  // the sequence and chunk of this record
-  int64_t seq, c, slot, t0, len;
-  if (tp.chunks) {
-    seq = rs / tp.chunks;
-  } else {
-    int before = 0;
-    for (int64_t i0 = 0; i0 < p.nseq; i0 += kPrepThreads) {
-      const int64_t i = i0 + pt;
-      before += __syncthreads_count(i < p.nseq && p.cu[i] / kC + i <= rs);
-    }
-    seq = before > 0 ? before - 1 : 0;
-  }
-  if (!gdr_sequence(p, seq, slot, t0, len)) return;
-  c = rs - first_slot(tp, seq, t0);
-  if (c < 0 || c * kC >= len) return;
-  const int64_t left = len - c * kC;
-  const int nv = (int)(left < kC ? left : kC);
-  t0 += c * kC;
-  const int64_t g = hd / (p.H / p.Hk);
-
   if (pt == 0) {
     mbar_init(&s.full, 1);
     mbar_init(&s.done, 1);
     fence_mbar_init();
-    mbar_expect_tx(&s.full, NP * 128 * 128);
-#pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      tma_load_3d(s.kq[n], &mK, &s.full, 64 * n, (int)g, (int)t0);
-      tma_load_3d(s.kq[n] + kC * 128, &mQ, &s.full, 64 * n, (int)g, (int)t0);
-    }
   }
-  __syncwarp();
   if (pw == 1) {
     tmem_alloc(&s.taddr, 64);
     tmem_relinquish();
   }
-  int64_t g63x = 0;
-  if (pw == 3) {  // the gates: lane l has tokens 2 l and 2 l + 1
-    float dtv[2] = {}, be[2] = {};
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (2 * lane + e < nv) {
-        const int64_t at = t0 + 2 * lane + e;
-        if (p.dt) dtv[e] = ld(static_cast<const __nv_bfloat16 *>(p.dt) + at * p.dt_row + hd);
-        be[e] = ld(static_cast<const __nv_bfloat16 *>(p.beta) + at * p.beta_row + hd);
-      }
-    }
-    const float Ah = p.dt ? p.A[hd] : 0.f;
-    const float bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
-    // log2 of the decays summed in fixed point, 2^-44 a unit: exact, and the
-    // sums of 64 fit (each at least -256: zero either way)
-    int64_t gs[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l2 = 0.f, b = 0.f;
-      if (2 * lane + e < nv) {
-        if (p.dt) {
-          float d = dtv[e] + bias;
-          if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
-          l2 = fmaxf(d * Ah * kLog2e, -256.f);
-        }
-        b = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be[e] * kLog2e)) : be[e];
-      }
-      gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
-      s.beta[2 * lane + e] = b;
-    }
-    int64_t sum = gs[0] + gs[1];
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += o;
-    }
-    g63x = __shfl_sync(0xffffffffu, sum, 31);
-    // hi: multiples of 2^-10 (24 bits); lo: the rest below, in 2^-34
-    auto parts = [](int64_t g) {
-      return mk2((float)(int)(g >> 34) * 0.0009765625f,
-                 (float)(int)((g & ((1ll << 34) - 1)) >> 10) * 5.8207660913467407e-11f);
-    };
-    s.g[2 * lane] = parts(sum - gs[1]);
-    s.g[2 * lane + 1] = parts(sum);
-  }
   tc_fence_before();
-  __syncthreads();  // the barriers, TMEM's address, the gates
+  __syncthreads();
   tc_fence_after();
   const uint32_t tb = s.taddr;
-  bool ok = mbar_wait(&s.full, 0, kWaitLimit);
-  if (pw == 0) {
-    if (elect_one()) {
-      const uint64_t d = smem_desc(smem_u32(s.kq[0]), 16, 1024, kSwizzle128B);
-#pragma unroll
-      for (int kk = 0; kk < KD / 16; ++kk) {
-        const uint64_t o = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
-        mma_ss(tb, d + o, d + o, idesc_bf16_f32(128, 64, false, false), kk > 0);
+  uint32_t ph = 0;
+  bool ok = true;
+  for (int64_t unit = blockIdx.x; unit < tp.units; unit += gridDim.x) {
+    // the sequence and chunk of this record
+    const int64_t hd = unit % p.H, rs = unit / p.H;
+    int64_t seq, c, slot, t0, len;
+    if (tp.chunks) {
+      seq = rs / tp.chunks;
+    } else {
+      int before = 0;
+      for (int64_t i0 = 0; i0 < p.nseq; i0 += kPrepThreads) {
+        const int64_t i = i0 + pt;
+        before += __syncthreads_count(i < p.nseq && p.cu[i] / kC + i <= rs);
       }
-      mma_commit(&s.done);
+      seq = before > 0 ? before - 1 : 0;
+    }
+    if (!gdr_sequence(p, seq, slot, t0, len)) continue;
+    c = rs - first_slot(tp, seq, t0);
+    if (c < 0 || c * kC >= len) continue;
+    const int64_t left = len - c * kC;
+    const int nv = (int)(left < kC ? left : kC);
+    t0 += c * kC;
+    const int64_t g = hd / (p.H / p.Hk);
+
+    if (pt == 0) {
+      // (the records before have left the shared memory)
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      mbar_expect_tx(&s.full, NP * 128 * 128);
+#pragma unroll
+      for (int n = 0; n < NP; ++n) {
+        tma_load_3d(s.kq[n], &mK, &s.full, 64 * n, (int)g, (int)t0);
+        tma_load_3d(s.kq[n] + kC * 128, &mQ, &s.full, 64 * n, (int)g, (int)t0);
+      }
     }
     __syncwarp();
-  }
-  {  // |q|^2, two threads a query (|k|^2 is on G's diagonal)
-    const int row = pt >> 1, hf = pt & 1;
-    f2 a = mk2(0.f, 0.f);
+    int64_t g63x = 0;
+    if (pw == 3) {  // the gates: lane l has tokens 2 l and 2 l + 1
+      float dtv[2] = {}, be[2] = {};
 #pragma unroll
-    for (int i = 0; i < KD / 16; ++i) {
-      const int ch = hf * (KD / 16) + i;
-      const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[ch >> 3][0] + sw128(kC + row, ch & 7));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) a = fma_bf16x2(w[e], w[e], a);
-    }
-    float n2 = a.x + a.y;
-    n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
-    if (hf == 0) s.qq[row] = n2;
-  }
-  ok = mbar_wait(&s.done, 0, kWaitLimit) && ok;
-  tc_fence_after();
-  __syncthreads();  // |q|^2; every thread is done with the rows
-
-  const int tok = pt & 63;
-  const bool isk = pt < 64, on = tok < nv;
-  const uint32_t grow = tb + ((uint32_t)(32 * pw) << 16);
-  // of G this row's columns of its own 32-token block; own: of its 16-token block
-  const int blk = pw & 1;
-  const bool up = lane >= 16;  // the second of the two 16-token blocks
-  uint32_t r0[16], own[16];
-  {
-    uint32_t r1[16];
-    tmem_ld16(grow + 32 * blk, r0);
-    tmem_ld16(grow + 32 * blk + 16, r1);
-    tmem_ld_wait();
-#pragma unroll
-    for (int q = 0; q < 16; ++q) own[q] = up ? r1[q] : r0[q];
-  }
-  float n2;
-  if (isk) {
-    uint32_t t[8];  // own[lane & 15], bit by bit of the index
-#pragma unroll
-    for (int q = 0; q < 8; ++q) t[q] = lane & 8 ? own[q + 8] : own[q];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) t[q] = lane & 4 ? t[q + 4] : t[q];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) t[q] = lane & 2 ? t[q + 2] : t[q];
-    n2 = __uint_as_float(lane & 1 ? t[1] : t[0]);
-  } else {
-    n2 = s.qq[tok];
-  }
-  // the row's power of two f = 2^-e, |row| f in 1 .. 2; its norm factor beside
-  // rows scaled so
-  int e = ((int)((__float_as_uint(n2) >> 23) & 255u) - 127) >> 1;
-  e = !(n2 > 0.f) ? 0 : e < -60 ? -60 : e > 60 ? 60 : e;
-  float f = 0.f, nf = 0.f;
-  if (on) {
-    f = pow2i(-e);
-    nf = pow2i(e);
-    if (p.flags & GDR_QK_L2NORM) {
-      const float a = n2 + p.l2_eps, r = rsqrtf(a);
-      // (one Newton step on the hardware's; infinite norms give 0)
-      nf = n2 == 0.f || !(r > 0.f) ? 0.f : nf * (r * fmaf(-0.5f * a * r, r, 1.5f));
-    }
-    if (n2 != n2) nf = n2;
-  }
-  const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
-  const float eg = ex2(gi.x + gi.y);
-  float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, ek) - kRecT));
-  float rowf = f;
-  if (isk) {
-    const float b = s.beta[tok];
-    rowf = nf * nf * b * f;
-    s.bv[tok] = nf * b;
-    fac[0 * kC + tok] = -nf * eg;                              // ek
-    fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
-    s.f[tok] = f;
-    s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
-    const float m = warp_max(2.f * nf * eg);
-    if (lane == 0) s.ekn[pw] = m;
-  } else {
-    fac[2 * kC + tok] = p.scale * nf;  // cq
-    fac[3 * kC + tok] = f * eg;        // fq
-  }
-  __syncthreads();  // f, h
-  if (hd % (p.H / p.Hk) == 0) {  // the keys, scaled; rows behind the end may hold anything
-    uint8_t *out = tp.keys + (rs * p.Hk + g) * (int64_t)(NP * kSlab);
-#pragma unroll
-    for (int i = 0; i < NP * 4; ++i) {
-      const int at = (i & 3) * kPrepThreads + pt;  // 16 bytes of the slab: any swizzle
-      const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[i >> 2][16 * at]);
-      const float fr = s.f[at >> 3];
-      const uint32_t f2x = __byte_perm(__float_as_uint(fr), 0, 0x3232);  // (a power of two: exact)
-      uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f2 y = fma_bf16x2(w[e], f2x, mk2(0.f, 0.f));
-        w[e] = (at >> 3) < nv ? pack_h2(y.x, y.y) : 0u;
+      for (int e = 0; e < 2; ++e) {
+        if (2 * lane + e < nv) {
+          const int64_t at = t0 + 2 * lane + e;
+          if (p.dt) dtv[e] = ld(static_cast<const __nv_bfloat16 *>(p.dt) + at * p.dt_row + hd);
+          be[e] = ld(static_cast<const __nv_bfloat16 *>(p.beta) + at * p.beta_row + hd);
+        }
       }
-      *reinterpret_cast<uint4 *>(out + (i >> 2) * kSlab + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+      const float Ah = p.dt ? p.A[hd] : 0.f;
+      const float bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
+      // log2 of the decays summed in fixed point, 2^-44 a unit: exact, and the
+      // sums of 64 fit (each at least -256: zero either way)
+      int64_t gs[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l2 = 0.f, b = 0.f;
+        if (2 * lane + e < nv) {
+          if (p.dt) {
+            float d = dtv[e] + bias;
+            if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
+            l2 = fmaxf(d * Ah * kLog2e, -256.f);
+          }
+          b = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be[e] * kLog2e)) : be[e];
+        }
+        gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
+        s.beta[2 * lane + e] = b;
+      }
+      int64_t sum = gs[0] + gs[1];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += o;
+      }
+      g63x = __shfl_sync(0xffffffffu, sum, 31);
+      // hi: multiples of 2^-10 (24 bits); lo: the rest below, in 2^-34
+      auto parts = [](int64_t g) {
+        return mk2((float)(int)(g >> 34) * 0.0009765625f,
+                   (float)(int)((g & ((1ll << 34) - 1)) >> 10) * 5.8207660913467407e-11f);
+      };
+      s.g[2 * lane] = parts(sum - gs[1]);
+      s.g[2 * lane + 1] = parts(sum);
     }
-    __syncthreads();  // A and P take the keys' place
-  }
+    ok = mbar_wait(&s.full, ph, kWaitLimit) && ok;
+    if (pw == 0) {
+      if (elect_one()) {
+        const uint64_t d = smem_desc(smem_u32(s.kq[0]), 16, 1024, kSwizzle128B);
+#pragma unroll
+        for (int kk = 0; kk < KD / 16; ++kk) {
+          const uint64_t o = (uint64_t)(((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4);
+          mma_ss(tb, d + o, d + o, idesc_bf16_f32(128, 64, false, false), kk > 0);
+        }
+        mma_commit(&s.done);
+      }
+      __syncwarp();
+    }
+    {  // |q|^2, two threads a query (|k|^2 is on G's diagonal)
+      const int row = pt >> 1, hf = pt & 1;
+      f2 a = mk2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < KD / 16; ++i) {
+        const int ch = hf * (KD / 16) + i;
+        const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[ch >> 3][0] + sw128(kC + row, ch & 7));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a = fma_bf16x2(w[e], w[e], a);
+      }
+      float n2 = a.x + a.y;
+      n2 += __shfl_xor_sync(0xffffffffu, n2, 1);
+      if (hf == 0) s.qq[row] = n2;
+    }
+    ok = mbar_wait(&s.done, ph, kWaitLimit) && ok;
+    ph ^= 1;
+    tc_fence_after();
+    __syncthreads();  // the gates, |q|^2; every thread is done with the rows
 
-  // A and P, 16 columns at a time.  In the row's own 16-token block the decays
-  // are taken element by element; in blocks before it they go by way of the
-  // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
-  // above 1.
-  uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
-  const bool part = nv < kC;
-  auto put = [&](int J, const f2(&x)[8]) {
-    f2 z[8];
+    const int tok = pt & 63;
+    const bool isk = pt < 64, on = tok < nv;
+    const uint32_t grow = tb + ((uint32_t)(32 * pw) << 16);
+    // of G this row's columns of its own 32-token block; own: of its 16-token block
+    const int blk = pw & 1;
+    const bool up = lane >= 16;  // the second of the two 16-token blocks
+    uint32_t r0[16], own[16];
+    {
+      uint32_t r1[16];
+      tmem_ld16(grow + 32 * blk, r0);
+      tmem_ld16(grow + 32 * blk + 16, r1);
+      tmem_ld_wait();
 #pragma unroll
-    for (int q = 0; q < 8; ++q) z[q] = part && !on ? mk2(0.f, 0.f) : x[q];  // (may hold anything)
-    if (isk) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
-            make_float4(z[2 * q].x, z[2 * q].y, z[2 * q + 1].x, z[2 * q + 1].y);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *reinterpret_cast<uint4 *>(P + sw128(tok, 2 * J + q)) =
-            make_uint4(pack_h2(z[4 * q].x, z[4 * q].y), pack_h2(z[4 * q + 1].x, z[4 * q + 1].y),
-                       pack_h2(z[4 * q + 2].x, z[4 * q + 2].y), pack_h2(z[4 * q + 3].x, z[4 * q + 3].y));
+      for (int q = 0; q < 16; ++q) own[q] = up ? r1[q] : r0[q];
     }
-  };
-  auto before = [&](int J, const uint32_t(&r)[16], f2(&x)[8]) {  // a block before the row's own
-    const f2 ge = s.g[16 * J + 15];
-    const float fr = rowf * ex2((gi.x - ge.x) + (gi.y - ge.y));
+    float n2;
+    if (isk) {
+      uint32_t t[8];  // own[lane & 15], bit by bit of the index
+#pragma unroll
+      for (int q = 0; q < 8; ++q) t[q] = lane & 8 ? own[q + 8] : own[q];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = lane & 4 ? t[q + 4] : t[q];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) t[q] = lane & 2 ? t[q + 2] : t[q];
+      n2 = __uint_as_float(lane & 1 ? t[1] : t[0]);
+    } else {
+      n2 = s.qq[tok];
+    }
+    // the row's power of two f = 2^-e, |row| f in 1 .. 2; its norm factor beside
+    // rows scaled so
+    int e = ((int)((__float_as_uint(n2) >> 23) & 255u) - 127) >> 1;
+    e = !(n2 > 0.f) ? 0 : e < -60 ? -60 : e > 60 ? 60 : e;
+    float f = 0.f, nf = 0.f;
+    if (on) {
+      f = pow2i(-e);
+      nf = pow2i(e);
+      if (p.flags & GDR_QK_L2NORM) {
+        const float a = n2 + p.l2_eps, r = rsqrtf(a);
+        // (one Newton step on the hardware's; infinite norms give 0)
+        nf = n2 == 0.f || !(r > 0.f) ? 0.f : nf * (r * fmaf(-0.5f * a * r, r, 1.5f));
+      }
+      if (n2 != n2) nf = n2;
+    }
+    const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
+    const float eg = ex2(gi.x + gi.y);
+    float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, ek) - kRecT));
+    float rowf = f;
+    if (isk) {
+      const float b = s.beta[tok];
+      rowf = nf * nf * b * f;
+      s.bv[tok] = nf * b;
+      fac[0 * kC + tok] = -nf * eg;                              // ek
+      fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
+      s.f[tok] = f;
+      s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
+      const float m = warp_max(2.f * nf * eg);
+      if (lane == 0) s.ekn[pw] = m;
+    } else {
+      fac[2 * kC + tok] = p.scale * nf;  // cq
+      fac[3 * kC + tok] = f * eg;        // fq
+    }
+    __syncthreads();  // f, h
+    if (hd % (p.H / p.Hk) == 0) {  // the keys, scaled; rows behind the end may hold anything
+      uint8_t *out = tp.keys + (rs * p.Hk + g) * (int64_t)(NP * kSlab);
+#pragma unroll
+      for (int i = 0; i < NP * 4; ++i) {
+        const int at = (i & 3) * kPrepThreads + pt;  // 16 bytes of the slab: any swizzle
+        const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[i >> 2][16 * at]);
+        const float fr = s.f[at >> 3];
+        const uint32_t f2x = __byte_perm(__float_as_uint(fr), 0, 0x3232);  // (a power of two: exact)
+        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f2 y = fma_bf16x2(w[e], f2x, mk2(0.f, 0.f));
+          w[e] = (at >> 3) < nv ? pack_h2(y.x, y.y) : 0u;
+        }
+        *reinterpret_cast<uint4 *>(out + (i >> 2) * kSlab + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncthreads();  // A and P take the keys' place
+    }
+
+    // A and P, 16 columns at a time.  In the row's own 16-token block the decays
+    // are taken element by element; in blocks before it they go by way of the
+    // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
+    // above 1.
+    uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
+    const bool part = nv < kC;
+    auto put = [&](int J, const f2(&x)[8]) {
+      f2 z[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) z[q] = part && !on ? mk2(0.f, 0.f) : x[q];  // (may hold anything)
+      if (isk) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
+              make_float4(z[2 * q].x, z[2 * q].y, z[2 * q + 1].x, z[2 * q + 1].y);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<uint4 *>(P + sw128(tok, 2 * J + q)) =
+              make_uint4(pack_h2(z[4 * q].x, z[4 * q].y), pack_h2(z[4 * q + 1].x, z[4 * q + 1].y),
+                         pack_h2(z[4 * q + 2].x, z[4 * q + 2].y), pack_h2(z[4 * q + 3].x, z[4 * q + 3].y));
+      }
+    };
+    auto before = [&](int J, const uint32_t(&r)[16], f2(&x)[8]) {  // a block before the row's own
+      const f2 ge = s.g[16 * J + 15];
+      const float fr = rowf * ex2((gi.x - ge.x) + (gi.y - ge.y));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 h = *reinterpret_cast<const float4 *>(&s.h[16 * J + 4 * q]);
+        x[2 * q] = mul2(mul2(mk2(h.x, h.y), mk2(fr, fr)),
+                        mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])));
+        x[2 * q + 1] = mul2(mul2(mk2(h.z, h.w), mk2(fr, fr)),
+                            mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+      }
+    };
+    {
+      f2 x[8];
+      float o[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int j = (tok & ~15) + q;
+        const f2 gj = s.g[j];
+        const f2 d = add2(gi, mk2(-gj.x, -gj.y));
+        const bool in = isk ? j < tok : j <= tok;
+        o[q] = in ? __uint_as_float(own[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
+      }
+      before(2 * blk, r0, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = up ? x[q] : mk2(o[2 * q], o[2 * q + 1]);
+      put(2 * blk, x);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = up ? mk2(o[2 * q], o[2 * q + 1]) : mk2(0.f, 0.f);
+      put(2 * blk + 1, x);
+    }
+#pragma unroll 1
+    for (int J = 0; J < 2; ++J) {
+      f2 x[8];
+      if (blk) {
+        tmem_ld16(grow + 16 * J, r0);
+        tmem_ld_wait();
+        before(J, r0, x);
+        put(J, x);
+      } else if (!isk) {  // above P's diagonal blocks
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = mk2(0.f, 0.f);
+        put(2 + J, x);
+      }
+    }
+    tc_fence_before();
+    // the chunk's decay multiplies the state once a chunk: exact (while the other
+    // warps invert)
+    double gtot = 0.;
+    if (pw == 3) gtot = exp2((double)g63x * 0x1p-44);
+    if (isk) {
+      // the inverses of this warp's two diagonal blocks, a column a lane
+      __syncwarp();
+      const int o = 32 * pw + (lane & 16), col = lane & 15;
+      f2 x[8];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        f2 a0 = mk2(col == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
+#pragma unroll
+        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
+          const float4 a = *reinterpret_cast<const float4 *>(&s.Am[o + i][o + 4 * j4]);
+          // (columns from i on hold zeros; x not yet set is not read)
+          if (4 * j4 + 1 < i) a0 = fma2(mk2(-a.x, -a.y), x[2 * j4], a0);
+          else a0.x = fmaf(-a.x, x[2 * j4].x, a0.x);
+          if (4 * j4 + 3 < i) a1 = fma2(mk2(-a.z, -a.w), x[2 * j4 + 1], a1);
+          else if (4 * j4 + 2 < i) a1.x = fmaf(-a.z, x[2 * j4 + 1].x, a1.x);
+        }
+        a0 = add2(a0, a1);
+        const float xi = a0.x + a0.y;
+        if (i & 1) x[i / 2].y = xi; else x[i / 2].x = xi;
+      }
+      __syncwarp();  // every lane has read the blocks
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s.Am[o + 2 * i][o + col] = x[i].x;
+        s.Am[o + 2 * i + 1][o + col] = x[i].y;
+      }
+    }
+    __syncthreads();
+    {  // below the diagonal blocks of 16: half pw & 1 of the columns of pair pw / 2
+      const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
+      float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
+      float c1[1][4], c2[1][4];
+      small_product<1, 2, false>(&s.Am[o + 16][o], &s.Am[o][o + n], pw & 1, c1);
+      put_product<1>(scratch, c1, 1.f);
+      __syncwarp();
+      small_product<1, 2, true>(&s.Am[o + 16][o + 16], scratch, 0, c2);
+      __syncthreads();  // A21 has been read
+      put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
+    }
+    __syncthreads();
+    {  // and of 32: eight columns a warp
+      float *scratch = &s.Am[0][32 + 8 * pw];
+      float c1[2][4], c2[2][4];
+      small_product<2, 4, false>(&s.Am[32][0], &s.Am[0][8 * pw], pw, c1);
+      put_product<2>(scratch, c1, 1.f);
+      __syncwarp();
+      small_product<2, 4, true>(&s.Am[32][32], scratch, 0, c2);
+      __syncthreads();
+      put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
+    }
+    __syncthreads();
+    // T diag(b) to float16 pairs: row pt / 2, half pt % 2
+    const int row = pt >> 1, hf = pt & 1;
+    const bool have = hf <= (row >> 5);
+    f2 t[16];
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (have) a = *reinterpret_cast<const float4 *>(&s.Am[row][32 * hf + 4 * q]);
+      const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
+      t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
+      t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
+      sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum = warp_max(sum);
+    if (lane == 0) s.tn[pw] = sum;
+    __syncthreads();  // T takes A's place
+    const float tn = fmaxf(fmaxf(s.tn[0], s.tn[1]), fmaxf(s.tn[2], s.tn[3]));
+    int eT = scale_exp(tn);
+    eT = eT < 0 ? eT : 0;
+    const f2 sc = mk2(pow2i(eT), pow2i(eT));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const float4 h = *reinterpret_cast<const float4 *>(&s.h[16 * J + 4 * q]);
-      x[2 * q] = mul2(mul2(mk2(h.x, h.y), mk2(fr, fr)),
-                      mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])));
-      x[2 * q + 1] = mul2(mul2(mk2(h.z, h.w), mk2(fr, fr)),
-                          mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+      uint4 hi, lo;
+      split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
+      split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
+      split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
+      split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
+      *reinterpret_cast<uint4 *>(s.T + sw128(row, 4 * hf + q)) = hi;
+      *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
     }
-  };
-  {
-    f2 x[8];
-    float o[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const int j = (tok & ~15) + q;
-      const f2 gj = s.g[j];
-      const f2 d = add2(gi, mk2(-gj.x, -gj.y));
-      const bool in = isk ? j < tok : j <= tok;
-      o[q] = in ? __uint_as_float(own[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
+    if (pw == 3 && lane == 0) {
+      fac[4 * kC] = (float)gtot;
+      fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
+      fac[4 * kC + 2] = tn * sc.x;
+      fac[4 * kC + 3] = (float)eT;
     }
-    before(2 * blk, r0, x);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = up ? x[q] : mk2(o[2 * q], o[2 * q + 1]);
-    put(2 * blk, x);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = up ? mk2(o[2 * q], o[2 * q + 1]) : mk2(0.f, 0.f);
-    put(2 * blk + 1, x);
-  }
-#pragma unroll 1
-  for (int J = 0; J < 2; ++J) {
-    f2 x[8];
-    if (blk) {
-      tmem_ld16(grow + 16 * J, r0);
-      tmem_ld_wait();
-      before(J, r0, x);
-      put(J, x);
-    } else if (!isk) {  // above P's diagonal blocks
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = mk2(0.f, 0.f);
-      put(2 + J, x);
-    }
-  }
-  tc_fence_before();
-  // the chunk's decay multiplies the state once a chunk: exact (while the other
-  // warps invert)
-  double gtot = 0.;
-  if (pw == 3) gtot = exp2((double)g63x * 0x1p-44);
-  if (isk) {
-    // the inverses of this warp's two diagonal blocks, a column a lane
-    __syncwarp();
-    const int o = 32 * pw + (lane & 16), col = lane & 15;
-    f2 x[8];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      f2 a0 = mk2(col == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
-#pragma unroll
-      for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-        const float4 a = *reinterpret_cast<const float4 *>(&s.Am[o + i][o + 4 * j4]);
-        // (columns from i on hold zeros; x not yet set is not read)
-        if (4 * j4 + 1 < i) a0 = fma2(mk2(-a.x, -a.y), x[2 * j4], a0);
-        else a0.x = fmaf(-a.x, x[2 * j4].x, a0.x);
-        if (4 * j4 + 3 < i) a1 = fma2(mk2(-a.z, -a.w), x[2 * j4 + 1], a1);
-        else if (4 * j4 + 2 < i) a1.x = fmaf(-a.z, x[2 * j4 + 1].x, a1.x);
-      }
-      a0 = add2(a0, a1);
-      const float xi = a0.x + a0.y;
-      if (i & 1) x[i / 2].y = xi; else x[i / 2].x = xi;
-    }
-    __syncwarp();  // every lane has read the blocks
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s.Am[o + 2 * i][o + col] = x[i].x;
-      s.Am[o + 2 * i + 1][o + col] = x[i].y;
-    }
-  }
-  __syncthreads();
-  {  // below the diagonal blocks of 16: half pw & 1 of the columns of pair pw / 2
-    const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
-    float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
-    float c1[1][4], c2[1][4];
-    small_product<1, 2, false>(&s.Am[o + 16][o], &s.Am[o][o + n], pw & 1, c1);
-    put_product<1>(scratch, c1, 1.f);
-    __syncwarp();
-    small_product<1, 2, true>(&s.Am[o + 16][o + 16], scratch, 0, c2);
-    __syncthreads();  // A21 has been read
-    put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
-  }
-  __syncthreads();
-  {  // and of 32: eight columns a warp
-    float *scratch = &s.Am[0][32 + 8 * pw];
-    float c1[2][4], c2[2][4];
-    small_product<2, 4, false>(&s.Am[32][0], &s.Am[0][8 * pw], pw, c1);
-    put_product<2>(scratch, c1, 1.f);
-    __syncwarp();
-    small_product<2, 4, true>(&s.Am[32][32], scratch, 0, c2);
+    fence_async_smem();
+    tc_fence_before();
     __syncthreads();
-    put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
+    tc_fence_after();
+    if (pt == 0) {
+      uint8_t *out = tp.rec + unit * (int64_t)sizeof(Rec);
+      bulk_store(out, s.T, kRecT);
+      bulk_store(out + kRecT, s.rest, sizeof(Rec) - kRecT);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
   }
-  __syncthreads();
-  // T diag(b) to float16 pairs: row pt / 2, half pt % 2
-  const int row = pt >> 1, hf = pt & 1;
-  const bool have = hf <= (row >> 5);
-  f2 t[16];
-  float sum = 0.f;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (have) a = *reinterpret_cast<const float4 *>(&s.Am[row][32 * hf + 4 * q]);
-    const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
-    t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
-    t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
-    sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
-  }
-  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-  sum = warp_max(sum);
-  if (lane == 0) s.tn[pw] = sum;
-  __syncthreads();  // T takes A's place
-  const float tn = fmaxf(fmaxf(s.tn[0], s.tn[1]), fmaxf(s.tn[2], s.tn[3]));
-  int eT = scale_exp(tn);
-  eT = eT < 0 ? eT : 0;
-  const f2 sc = mk2(pow2i(eT), pow2i(eT));
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint4 hi, lo;
-    split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
-    split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
-    split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
-    split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
-    *reinterpret_cast<uint4 *>(s.T + sw128(row, 4 * hf + q)) = hi;
-    *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
-  }
-  if (pw == 3 && lane == 0) {
-    fac[4 * kC] = (float)gtot;
-    fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
-    fac[4 * kC + 2] = tn * sc.x;
-    fac[4 * kC + 3] = (float)eT;
-  }
-  fence_async_smem();
   if (!ok && tp.status) atomicExch(tp.status, 1);
-  tc_fence_before();
+  if (pt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncthreads();
-  tc_fence_after();
   if (pw == 1) tmem_dealloc(tb, 64);
-  if (pt == 0) {
-    uint8_t *out = tp.rec + (rs * p.H + hd) * (int64_t)sizeof(Rec);
-    bulk_store(out, s.T, kRecT);
-    bulk_store(out + kRecT, s.rest, sizeof(Rec) - kRecT);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  }
 }
 
 // ------------------------------------------------------------- the chain
@@ -1263,7 +1275,8 @@ cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMa
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(gdr_tc_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  gdr_prep_kernel<KD><<<(unsigned)(slots_of(q.p) * q.p.H), kPrepThreads, prep, s>>>(mK, mQ, q);
+  const int64_t most = 6ll * device_sm_count();
+  gdr_prep_kernel<KD><<<(unsigned)(q.units < most ? q.units : most), kPrepThreads, prep, s>>>(mK, mQ, q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(gdr_tc_kernel<KD>, dim3((unsigned)(q.p.nseq * q.p.H * q.vtiles)),
@@ -1288,6 +1301,7 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   GdrTcParams q;
   q.p = p;
   q.vtiles = (p.V + kV - 1) / kV;
+  q.units = slots_of(p) * p.H;
   q.chunks = p.cu ? 0 : (p.L + kC - 1) / kC;
   q.rec = static_cast<uint8_t *>(workspace) + kGdrStatusBytes;
   q.keys = q.rec + (size_t)(slots_of(p) * p.H) * sizeof(Rec);
