@@ -68,8 +68,10 @@ struct Rec {
   uint8_t P[kC * 128];
   float ek[kC], cu[kC], cq[kC];  // factors of KS (negative), U' and y
   float fq[kC];                  // of queries: powers of two and decays
-  float gC, ekn, tn, eT;         // e^g_63; bounds of ek |k| and of T's rows (scaled); T's exponent
-  float pad[12];
+  // e^g_63; bounds of ek |k| and of T's rows (scaled); T's exponent; the largest
+  // write strength, at least 1, of a chunk that contracts the state, or 0
+  float gC, ekn, tn, eT, con;
+  float pad[11];
 };
 // and, for a chunk and key head, the keys as scaled float16: KD / 64 slabs of
 // 64 x 64, 128-byte swizzled rows.
@@ -335,6 +337,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
     }
     __syncwarp();
     int64_t g63x = 0;
+    float con = 0.f;
     if (pw == 3) {  // the gates: lane l has tokens 2 l and 2 l + 1
       float dtv[2] = {}, be[2] = {};
 #pragma unroll
@@ -350,6 +353,8 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       // log2 of the decays summed in fixed point, 2^-44 a unit: exact, and the
       // sums of 64 fit (each at least -256: zero either way)
       int64_t gs[2];
+      bool fine = (p.flags & GDR_QK_L2NORM) != 0;
+      float bmax = 1.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float l2 = 0.f, b = 0.f;
@@ -363,7 +368,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
         }
         gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
         s.beta[2 * lane + e] = b;
+        fine = fine && l2 <= 0.f && b >= 0.f && b <= 2.f;
+        bmax = fmaxf(bmax, b);
       }
+      fine = __all_sync(0xffffffffu, fine);
+      con = fine ? warp_max(bmax) : 0.f;
       int64_t sum = gs[0] + gs[1];
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -397,7 +406,8 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       f2 a = mk2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < KD / 16; ++i) {
-        const int ch = hf * (KD / 16) + i;
+        // (the halves' accesses lie in different banks)
+        const int ch = NP == 2 ? 8 * hf + (i ^ (4 * hf)) : hf * (KD / 16) + i;
         const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[ch >> 3][0] + sw128(kC + row, ch & 7));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -618,43 +628,47 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
     }
     __syncthreads();
-    // T diag(b) to float16 pairs: row pt / 2, half pt % 2
-    const int row = pt >> 1, hf = pt & 1;
-    const bool have = hf <= (row >> 5);
+    // T diag(b) to float16 pairs: row pt % 64, half pt / 64 (of the first rows
+    // the second half is zero)
+    const int hf = pw >> 1;
+    const bool have = pw != 2;
     f2 t[16];
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (have) a = *reinterpret_cast<const float4 *>(&s.Am[row][32 * hf + 4 * q]);
+      if (have) a = *reinterpret_cast<const float4 *>(&s.Am[tok][32 * hf + 4 * q]);
       const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
       t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
       t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
       sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum = warp_max(sum);
     if (lane == 0) s.tn[pw] = sum;
     __syncthreads();  // T takes A's place
-    const float tn = fmaxf(fmaxf(s.tn[0], s.tn[1]), fmaxf(s.tn[2], s.tn[3]));
+    // (a bound of the rows' sums: the largest of each half)
+    const float tn = fmaxf(s.tn[0], s.tn[1]) + fmaxf(s.tn[2], s.tn[3]);
     int eT = scale_exp(tn);
     eT = eT < 0 ? eT : 0;
     const f2 sc = mk2(pow2i(eT), pow2i(eT));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      uint4 hi, lo;
-      split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
-      split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
-      split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
-      split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
-      *reinterpret_cast<uint4 *>(s.T + sw128(row, 4 * hf + q)) = hi;
-      *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(row, 4 * hf + q)) = lo;
+      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+      if (have) {
+        split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
+        split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
+        split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
+        split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
+      }
+      *reinterpret_cast<uint4 *>(s.T + sw128(tok, 4 * hf + q)) = hi;
+      *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(tok, 4 * hf + q)) = lo;
     }
     if (pw == 3 && lane == 0) {
       fac[4 * kC] = (float)gtot;
       fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
       fac[4 * kC + 2] = tn * sc.x;
       fac[4 * kC + 3] = (float)eT;
+      fac[4 * kC + 4] = con;
     }
     fence_async_smem();
     tc_fence_before();
@@ -1048,12 +1062,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         mx = warp_max(mx);
-        // with m the state's largest value: |R| max(1, row sum of T) <= x + y m,
-        // and the next state's <= z + w m
-        const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn * kNorm;
-        if (lane == 0)
-          s.bound[c % 3][quarter] =
-              make_float4(t1 * mx, t1 * en, 128.f * tn * mx, fmaf(128.f * tn, en, fabsf(rc.gC)));
+        // From m, the largest value of the state entering the chunk, bounds of the
+        // state and U' leaving it, z + w m = n, and from such an n of the chunk
+        // before, bounds of this chunk's R and U, x + y n.  With keys of length at
+        // most 1, write strengths b in 0 .. 2 and no growth, I - b k k^T lengthens
+        // nothing: |S| <= e^g sqrt(K) m + 64 b |v| column by column, |R| <= |v| + |S|
+        // and |U| <= b (|v| + |S|).  Else step by step: |R| <= |v| + |ek k| sqrt(K) m,
+        // |U| <= (T's row sums) |R|, |dS| <= sum |k| |U'| <= 128 |U|.
+        const float b = rc.con;
+        float4 f = make_float4(65.f * b * b * mx, b, 65.f * b * b * mx, b * kNorm * rc.gC);
+        if (!(b > 0.f)) {
+          const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn * kNorm;
+          f = make_float4(t1 * mx, t1 * en, 128.f * tn * mx, fmaf(128.f * tn, en, fabsf(rc.gC)));
+        }
+        if (lane == 0) s.bound[c % 3][quarter] = f;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.conv[c % 3]);
@@ -1074,10 +1096,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) s.smax[quarter][ch] = m;
     pair_sync(quarter);
     float smax = fmaxf(s.smax[quarter][0], s.smax[quarter][1]);
-    // One scale 2^e a chunk for S, R and U.  |R| <= max |v| + |ek k| sqrt(K)
-    // max |S|, |U| <= (T's row sums) max |R|, |dS| <= sum |k| |U'| <= 128 max |U|.
+    // One scale 2^e a chunk for S, R and U, from the bounds beside the conversion.
     wait(&s.conv[0], 0, 13);
-    int eS = scale_exp(fmaxf(smax, fmaf(s.bound[0][quarter].y, smax, s.bound[0][quarter].x)));
+    int eS = scale_exp(fmaxf(smax, fmaf(s.bound[0][quarter].y, kNorm * smax, s.bound[0][quarter].x)));
     // S's pieces, hi and lo of 32 values within their own dS columns
     const uint32_t mycol = tb + lane_base + kColS + ch * KH;
     {
