@@ -6,27 +6,36 @@
 // inputs before a sequence's first token from its state (zeros without one),
 // the state left holding the sequence's last W - 1 inputs.
 //
-// Bound by its bytes.  A thread takes V consecutive channels over a run of
-// kRun tokens of one sequence, the W - 1 previous inputs in registers, kBatch
-// rows loaded together.  Runs are numbered so that every sequence starts a run
-// of its own without a scan over the lengths: sequence i, from row s_i, has
-// the runs floor(s_i / kRun) + i and on, which leaves it at least
-// ceil(len / kRun); a thread finds its sequence by bisection.  The thread
-// with a sequence's first run is the only one that touches its state: it
-// reads the old inputs, and takes the new ones from x, so no other thread's
-// order matters and one launch does.
+// Bound by its bytes.  A thread takes V consecutive channels over a run of RUN
+// tokens of one sequence, the W - 1 previous inputs in registers.  Runs are
+// numbered so that every sequence starts a run of its own without a scan over
+// the lengths: sequence i, from row s_i, has the runs floor(s_i / RUN) + i and
+// on, which leaves it at least ceil(len / RUN); a CTA's run is one, and each
+// warp looks for its sequence together.  The thread with a sequence's first
+// run is the only one that touches its state: it reads the old inputs, and
+// takes the new ones from x, so no other thread's order matters and one launch
+// does.
+//
+// Two forms.  Runs of 64 tokens are copied ahead into the thread's own
+// shared-memory slots (three batches of eight, as ssm_conv1d_fwd, whose
+// arithmetic this is bit for bit).  Sequences of under 16 tokens on average (a
+// decode batch) take runs of 8 through registers, four channels a thread: the
+// other form's 49 KB of slots and 8-channel registers leave too few threads in
+// flight to cover the latency of finding the sequence, its state and its row.
 #include "common.cuh"
 #include "internal.h"
 
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 128, kRun = 32, kBatch = 8;
+constexpr int kThreads = 128, kBatch = 8, kStages = 3;
+constexpr int kLong = 64, kShort = 8;  // tokens a run
 
 template <typename T, int V> struct Vec {  // V = 1
   using Raw = T;
   static __device__ __forceinline__ void widen(const Raw &w, float (&f)[V]) { f[0] = ld(&w); }
   static __device__ __forceinline__ Raw zero() { return T(0.f); }
+  static __device__ __forceinline__ Raw load(const T *p) { return *p; }
   static __device__ __forceinline__ void store(T *p, const float (&f)[V]) { st(p, f[0]); }
 };
 template <> struct Vec<__nv_bfloat16, 8> {
@@ -36,10 +45,26 @@ template <> struct Vec<__nv_bfloat16, 8> {
     f[4] = bf16lo(w.z); f[5] = bf16hi(w.z); f[6] = bf16lo(w.w); f[7] = bf16hi(w.w);
   }
   static __device__ __forceinline__ Raw zero() { return make_uint4(0u, 0u, 0u, 0u); }
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) {
+    return __ldcs(reinterpret_cast<const uint4 *>(p));
+  }
   static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[8]) {
     __stcs(reinterpret_cast<uint4 *>(p),
            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7])));
+  }
+};
+template <> struct Vec<__nv_bfloat16, 4> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void widen(const Raw &w, float (&f)[4]) {
+    f[0] = bf16lo(w.x); f[1] = bf16hi(w.x); f[2] = bf16lo(w.y); f[3] = bf16hi(w.y);
+  }
+  static __device__ __forceinline__ Raw zero() { return make_uint2(0u, 0u); }
+  static __device__ __forceinline__ Raw load(const __nv_bfloat16 *p) {
+    return __ldcs(reinterpret_cast<const uint2 *>(p));
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[4]) {
+    __stcs(reinterpret_cast<uint2 *>(p), make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])));
   }
 };
 template <> struct Vec<float, 4> {
@@ -48,6 +73,9 @@ template <> struct Vec<float, 4> {
     f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
   }
   static __device__ __forceinline__ Raw zero() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+  static __device__ __forceinline__ Raw load(const float *p) {
+    return __ldcs(reinterpret_cast<const float4 *>(p));
+  }
   static __device__ __forceinline__ void store(float *p, const float (&f)[4]) {
     __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
   }
@@ -82,49 +110,111 @@ template <int N> __device__ __forceinline__ void store_floats(float *p, const fl
   }
 }
 
-template <typename T, int V, int W, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPackedParams p) {
-  using Vc = Vec<T, V>;
-  constexpr int B = W - 1;  // inputs before a token
-  const int64_t chunks = (p.Cc + V - 1) / V;
-  const int64_t ch = ((int64_t)blockIdx.x * kThreads + threadIdx.x);
-  const int64_t run = (int64_t)blockIdx.y + (int64_t)blockIdx.z * 65535;
-  if (ch >= chunks || run >= p.tokens / kRun + p.nseq) return;
-  const int64_t c = ch * V;
-  // the last sequence whose first run is not after this one
+// The last sequence whose first run is not after `run`, by a whole warp: up to
+// 1024 sequences by counting (one round of loads), more by bisection.
+template <int RUN>
+__device__ __forceinline__ int64_t find_sequence(const ConvPackedParams &p, int64_t run) {
+  if (p.nseq <= 1024) {
+    int n = 0;
+    for (int i = threadIdx.x & 31; i < (int)p.nseq; i += 32) n += (int64_t)p.cu[i] / RUN + i <= run;
+    n = __reduce_add_sync(0xffffffffu, n);
+    return n > 0 ? n - 1 : 0;
+  }
   int64_t lo = 0, hi = p.nseq - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
-    if ((int64_t)p.cu[mid] / kRun + mid <= run) lo = mid;
+    if ((int64_t)p.cu[mid] / RUN + mid <= run) lo = mid;
     else hi = mid - 1;
   }
-  const int64_t begin = p.cu[lo], end = p.cu[lo + 1];
-  const int64_t j = run - (begin / kRun + lo);
+  return lo;
+}
+
+template <int BYTES> __device__ __forceinline__ void cp_async(void *dst, const void *src) {
+  const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+
+template <typename T, int V, int W, int RUN, bool SILU>
+__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPackedParams p) {
+  using Vc = Vec<T, V>;
+  using Raw = typename Vc::Raw;
+  constexpr int B = W - 1;  // inputs before a token
+  constexpr bool kAhead = RUN == kLong && V > 1;
+  __shared__ Raw stage[kAhead ? kStages : 1][kAhead ? kBatch : 1][kAhead ? kThreads : 1];
+  const int tid = threadIdx.x;
+  const int64_t run = (int64_t)blockIdx.y + (int64_t)blockIdx.z * 65535;
+  if (run >= p.tokens / RUN + p.nseq) return;
+  const int64_t seq = find_sequence<RUN>(p, run);
+  const int64_t c = ((int64_t)blockIdx.x * kThreads + tid) * V;
+  if (c >= p.Cc) return;
+  const int64_t begin = p.cu[seq], end = p.cu[seq + 1];
+  const int64_t j = run - (begin / RUN + seq);
   if (begin < 0 || end < begin || end > p.tokens || j < 0) return;
-  const int64_t slot = p.slots ? (int64_t)p.slots[lo] : lo;
+  const int64_t slot = p.slots ? (int64_t)p.slots[seq] : seq;
   if (p.slots && (slot < 0 || slot >= p.state_rows)) return;
-  const int64_t t0 = begin + j * kRun;
-  const int64_t t1 = t0 + kRun < end ? t0 + kRun : end;
+  const int64_t t0 = begin + j * RUN;
+  const int64_t t1 = t0 + RUN < end ? t0 + RUN : end;
   if (t0 >= t1) return;  // an empty sequence keeps its state
+  const int n = (int)(t1 - t0);
 
   const T *x = static_cast<const T *>(p.x) + c;
-  using Raw = typename Vc::Raw;
-  float win[B > 0 ? B : 1][V];
+  const T *px = x + t0 * p.x_row;
+  int at = 0;  // tokens copied
+  auto issue = [&](int k) {
+#pragma unroll
+    for (int a = 0; a < kBatch; ++a, ++at)
+      if (at < n) cp_async<sizeof(Raw)>(&stage[k][a][tid], px + at * p.x_row);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) issue(k);
+  }
+
+  // Channel pairs (each lane of a pair is exactly the scalar fmaf / multiply);
+  // V = 1 leaves the second lane unused.
+  constexpr int VP = (V + 1) / 2;
+  f2 w[VP][W], bias[VP], hist[B > 0 ? B : 1][VP];  // hist: oldest first
+  {
+    float f[V * W];
+    load_floats(p.w + c * W, f);
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+#pragma unroll
+      for (int q = 0; q < W; ++q) w[e][q] = mk2(f[2 * e * W + q], V > 1 ? f[((2 * e + 1) % V) * W + q] : 0.f);
+      bias[e] = p.bias ? mk2(__ldg(p.bias + c + 2 * e), V > 1 ? __ldg(p.bias + c + 2 * e + 1) : 0.f)
+                       : mk2(0.f, 0.f);
+    }
+  }
+  auto pairs = [](const float(&f)[V], f2(&h)[VP]) {
+#pragma unroll
+    for (int e = 0; e < VP; ++e) h[e] = mk2(f[2 * e], V > 1 ? f[(2 * e + 1) % V] : 0.f);
+  };
   if constexpr (B > 0) {
     if (j > 0) {
 #pragma unroll
-      for (int q = 0; q < B; ++q)
-        Vc::widen(*reinterpret_cast<const Raw *>(x + (t0 - B + q) * p.x_row), win[q]);
+      for (int q = 0; q < B; ++q) {
+        float f[V];
+        Vc::widen(Vc::load(x + (t0 - B + q) * p.x_row), f);
+        pairs(f, hist[q]);
+      }
     } else {
-      float old[V * B];
+      float old[V * B];  // the state's layout: a channel's inputs, oldest first
 #pragma unroll
       for (int i = 0; i < V * B; ++i) old[i] = 0.f;
       float *sp = p.state ? p.state + (slot * p.Cc + c) * B : nullptr;
       if (sp) load_floats(sp, old);
 #pragma unroll
-      for (int q = 0; q < B; ++q)
+      for (int q = 0; q < B; ++q) {
+        float f[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) win[q][e] = old[e * B + q];
+        for (int e = 0; e < V; ++e) f[e] = old[e * B + q];
+        pairs(f, hist[q]);
+      }
       if (sp) {  // the last B inputs: of x, or of the old state where the sequence is shorter
         const int64_t len = end - begin;
         float now[V * B];
@@ -140,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPacke
               f[e] = 0.f;
 #pragma unroll
               for (int o = 0; o < B; ++o)
-                if (o == B + t) f[e] = win[o][e];
+                if (o == B + t) f[e] = old[e * B + o];
             }
           }
 #pragma unroll
@@ -150,70 +240,100 @@ __global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPacke
       }
     }
   }
-  float w[V * W], bias[V];
-  load_floats(p.w + c * W, w);
+  T *u = static_cast<T *>(p.u) + t0 * p.Cc + c;
+  auto token = [&](const Raw &raw) {
+    float f[V], o[V];
+    Vc::widen(raw, f);
+    f2 xv[VP];
+    pairs(f, xv);
 #pragma unroll
-  for (int e = 0; e < V; ++e) bias[e] = p.bias ? __ldg(p.bias + c + e) : 0.f;
-  T *u = static_cast<T *>(p.u) + c;
-  for (int64_t t = t0; t < t1; t += kBatch) {
-    Raw raw[kBatch];
+    for (int e = 0; e < VP; ++e) {
+      f2 acc = fma2(w[e][W - 1], xv[e], bias[e]);  // the newest input first
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      raw[i] = t + i < t1 ? __ldcs(reinterpret_cast<const Raw *>(x + (t + i) * p.x_row)) : Vc::zero();
+      for (int q = B - 1; q >= 0; --q) acc = fma2(w[e][q], hist[q][e], acc);
+      o[2 * e] = SILU ? gate<T>(acc.x) : acc.x;
+      if (V > 1) o[(2 * e + 1) % V] = SILU ? gate<T>(acc.y) : acc.y;
+    }
+    Vc::store(u, o);
+    u += p.Cc;
+    if constexpr (B > 0) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (t + i >= t1) break;
-      float f[V], o[V];
-      Vc::widen(raw[i], f);
+      for (int e = 0; e < VP; ++e) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {  // the newest input first, as ssm_conv1d_fwd
-        float acc = fmaf(w[e * W + W - 1], f[e], bias[e]);
-#pragma unroll
-        for (int q = B - 1; q >= 0; --q) acc = fmaf(w[e * W + q], win[q][e], acc);
-        o[e] = SILU ? gate<T>(acc) : acc;
+        for (int q = 0; q + 1 < B; ++q) hist[q][e] = hist[q + 1][e];
+        hist[B - 1][e] = xv[e];
       }
-      Vc::store(u + (t + i) * p.Cc, o);
-      if constexpr (B > 0) {
+    }
+  };
+  if constexpr (kAhead) {
+    int k = 0;
+    for (int t = 0; t < n; t += kBatch) {
+      issue(k == 0 ? kStages - 1 : k - 1);  // the slots of the batch before
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
 #pragma unroll
-        for (int q = 0; q + 1 < B; ++q)
+      for (int a = 0; a < kBatch; ++a) {
+        if (t + a >= n) break;
+        token(stage[k][a][tid]);
+      }
+      k = k == kStages - 1 ? 0 : k + 1;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+  } else {
+    for (int t = 0; t < n; t += kBatch) {
+      Raw raw[kBatch];
 #pragma unroll
-          for (int e = 0; e < V; ++e) win[q][e] = win[q + 1][e];
+      for (int a = 0; a < kBatch; ++a) raw[a] = t + a < n ? Vc::load(px + (t + a) * p.x_row) : Vc::zero();
 #pragma unroll
-        for (int e = 0; e < V; ++e) win[B - 1][e] = f[e];
+      for (int a = 0; a < kBatch; ++a) {
+        if (t + a >= n) break;
+        token(raw[a]);
       }
     }
   }
 }
 
-template <typename T, int V, int W>
+template <typename T, int V, int W, int RUN>
 cudaError_t run_w(const ConvPackedParams &p, cudaStream_t s) {
-  const int64_t chunks = (p.Cc + V - 1) / V, runs = p.tokens / kRun + p.nseq;
+  const int64_t chunks = (p.Cc + V - 1) / V, runs = p.tokens / RUN + p.nseq;
   const int64_t gy = runs < 65535 ? runs : 65535, gz = (runs + 65534) / 65535;
   if (gz > 65535) return cudaErrorNotSupported;
   const dim3 grid((unsigned)((chunks + kThreads - 1) / kThreads), (unsigned)gy, (unsigned)gz);
-  if (p.silu) conv1d_packed_kernel<T, V, W, true><<<grid, kThreads, 0, s>>>(p);
-  else conv1d_packed_kernel<T, V, W, false><<<grid, kThreads, 0, s>>>(p);
+  if (p.silu) conv1d_packed_kernel<T, V, W, RUN, true><<<grid, kThreads, 0, s>>>(p);
+  else conv1d_packed_kernel<T, V, W, RUN, false><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
-template <typename T, int V>
+template <typename T, int V, int RUN>
 cudaError_t run_v(const ConvPackedParams &p, cudaStream_t s) {
+  if constexpr (RUN == kLong && V > 1) {
+    // (several CTAs' slots on an SM need the shared-memory carve-out, a
+    // preference of the current device: never fail the call on it)
+    const void *k = p.silu ? (const void *)conv1d_packed_kernel<T, V, 4, RUN, true>
+                           : (const void *)conv1d_packed_kernel<T, V, 4, RUN, false>;
+    if (p.W == 4 && cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+      cudaGetLastError();
+  }
   switch (p.W) {
-    case 1: return run_w<T, V, 1>(p, s);
-    case 2: return run_w<T, V, 2>(p, s);
-    case 3: return run_w<T, V, 3>(p, s);
-    default: return run_w<T, V, 4>(p, s);
+    case 1: return run_w<T, V, 1, RUN>(p, s);
+    case 2: return run_w<T, V, 2, RUN>(p, s);
+    case 3: return run_w<T, V, 3, RUN>(p, s);
+    default: return run_w<T, V, 4, RUN>(p, s);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_conv1d_packed(const ConvPackedParams &p, cudaStream_t s) {
-  // whole 16-byte vectors of x's and u's rows, or value by value
-  if (p.io == 1)
-    return p.Cc % 8 == 0 && p.x_row % 8 == 0 ? run_v<__nv_bfloat16, 8>(p, s)
-                                             : run_v<__nv_bfloat16, 1>(p, s);
-  return p.Cc % 4 == 0 && p.x_row % 4 == 0 ? run_v<float, 4>(p, s) : run_v<float, 1>(p, s);
+  // whole vectors of x's and u's rows, or value by value
+  const bool brief = p.tokens < 16 * p.nseq;
+  if (p.io == 1) {
+    if (p.Cc % 8 == 0 && p.x_row % 8 == 0)
+      return brief ? run_v<__nv_bfloat16, 4, kShort>(p, s) : run_v<__nv_bfloat16, 8, kLong>(p, s);
+    return brief ? run_v<__nv_bfloat16, 1, kShort>(p, s) : run_v<__nv_bfloat16, 1, kLong>(p, s);
+  }
+  if (p.Cc % 4 == 0 && p.x_row % 4 == 0)
+    return brief ? run_v<float, 4, kShort>(p, s) : run_v<float, 4, kLong>(p, s);
+  return brief ? run_v<float, 1, kShort>(p, s) : run_v<float, 1, kLong>(p, s);
 }
 
 }  // namespace ssm

@@ -430,7 +430,16 @@ def _scope(t, stream):
 
 def _elsewhere(t, stream):
     """Whether a call on ``t`` needs _scope."""
-    return stream is not None or (t.is_cuda and t.device.index != torch.cuda.current_device())
+    return stream is not None or (t.is_cuda and t.get_device() != torch._C._cuda_getDevice())
+
+
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _raw_stream(t):
+    """Handle of the current stream of ``t``'s device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _rows(t, inner, align):
@@ -441,6 +450,12 @@ def _rows(t, inner, align):
     if t.is_contiguous():
         return (t if aligned else t.clone()), 0
     shape, strides, lead = t.shape, t.stride(), t.dim() - inner
+    if aligned and inner == 2 and lead == 1:  # [b, heads, dim], the usual slice
+        row, want = strides[0], shape[1] * shape[2]
+        if strides[2] == 1 and strides[1] == shape[2] and row >= want:
+            return t, row
+    elif aligned and inner == 1 and lead == 1 and strides[1] == 1 and strides[0] >= shape[1]:
+        return t, strides[0]
     want, row = 1, 0
     for i in range(t.dim() - 1, -1, -1):
         if shape[i] == 1:
@@ -455,7 +470,7 @@ def _rows(t, inner, align):
 
 
 def _expect(name, t, dtype, shape, device):
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device):
         return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -474,7 +489,8 @@ def _own(name, t):
 
 def _gdr_inputs(q, k, v, dt, A, beta, dt_bias):
     """Checks the tensors a scan and a step share; returns their sizes."""
-    lead, (hk, K), (h, V) = tuple(v.shape[:-2]), q.shape[-2:], v.shape[-2:]
+    *lead, h, V = v.shape
+    lead, hk, K = tuple(lead), q.shape[-2], q.shape[-1]
     dev, io = v.device, v.dtype
     _expect("q", q, io, lead + (hk, K), dev)
     _expect("k", k, io, lead + (hk, K), dev)
@@ -546,20 +562,21 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
     y = torch.empty((b, Lq, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
     h_last = (torch.empty((n, h, K, V), dtype=torch.float32, device=dev) if h_last is None
               else _own("h_last", h_last))
-    a = L.GdrScanArgs(b, Lq, h, hk, K, V, n, rows, q_row, k_row, v_row, dt_row, beta_row,
-                      _io_of(v), flags, K ** -0.5 if scale is None else scale, l2_eps, _ptr(q),
-                      _ptr(k), _ptr(v), _ptr(dt), _ptr(beta), _ptr(_dense(A)),
-                      _ptr(_dense(dt_bias)), _ptr(h0), _ptr(_dense(cu_seqlens)),
-                      _ptr(_dense(slots)), _ptr(y), _ptr(h_last), None, 0)
-    lib = L.lib()
+    A, dt_bias = _dense(A), _dense(dt_bias)
+    cu_seqlens, slots = _dense(cu_seqlens), _dense(slots)
+    fields = (b, Lq, h, hk, K, V, n, rows, q_row, k_row, v_row, dt_row, beta_row, _io_of(v), flags,
+              K ** -0.5 if scale is None else scale, l2_eps, q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), _at(dt), beta.data_ptr(), _at(A), _at(dt_bias), _at(h0),
+              _at(cu_seqlens), _at(slots), y.data_ptr(), h_last.data_ptr())
     nbytes = ctypes.c_size_t(0)
-    L.check(lib.gdr_chunk_scan_workspace(ctypes.byref(a), ctypes.byref(nbytes)),
+    L.check(L.packed("gdr_chunk_scan_workspace")(L.GDR_SCAN(*fields, 0, 0), ctypes.addressof(nbytes)),
             "gdr_chunk_scan_workspace")
     if nbytes.value:
         workspace = _workspace(nbytes.value, workspace, dev)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), nbytes.value
-    st = _stream(None, dev)
-    L.check(lib.gdr_chunk_scan_fwd(ctypes.byref(a), st), "gdr_chunk_scan_fwd")
+    st = _raw_stream(y)
+    L.check(L.packed("gdr_chunk_scan_fwd")(
+        L.GDR_SCAN(*fields, workspace.data_ptr() if nbytes.value else 0, nbytes.value), st),
+        "gdr_chunk_scan_fwd")
     if nbytes.value and n and (check or sg or _CHECK_ALL):
         _check_status(workspace, st, "gdr_chunk_scan_fwd")
     if sg is None:
@@ -610,11 +627,12 @@ def gdr_scan_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, flag
     dt, dt_row = (None, 0) if dt is None else _rows(dt, 1, dt.element_size())
     beta, beta_row = _rows(beta, 1, beta.element_size())
     y = torch.empty((b, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
-    a = L.GdrStepArgs(b, h, hk, K, V, rows, q_row, k_row, v_row, dt_row, beta_row, _io_of(v),
-                      flags, K ** -0.5 if scale is None else scale, l2_eps, _ptr(q), _ptr(k),
-                      _ptr(v), _ptr(dt), _ptr(beta), _ptr(_dense(A)), _ptr(_dense(dt_bias)),
-                      _ptr(_dense(slots)), _ptr(state), _ptr(y))
-    L.check(L.lib().gdr_scan_step(ctypes.byref(a), _stream(None, dev)), "gdr_scan_step")
+    A, dt_bias, slots = _dense(A), _dense(dt_bias), _dense(slots)
+    L.check(L.packed("gdr_scan_step")(
+        L.GDR_STEP(b, h, hk, K, V, rows, q_row, k_row, v_row, dt_row, beta_row, _io_of(v), flags,
+                   K ** -0.5 if scale is None else scale, l2_eps, q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), _at(dt), beta.data_ptr(), _at(A), _at(dt_bias), _at(slots),
+                   state.data_ptr(), y.data_ptr()), _raw_stream(y)), "gdr_scan_step")
     if sg is None:
         return y
     return _home(sg, (host_y, host_state), (y, state))[0]
@@ -645,10 +663,10 @@ def gdr_gated_rmsnorm_fwd(x, z=None, weight=None, eps=1e-5, *, out=None, stream=
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     x = _own("out", out) if x is out else x.contiguous()
     tokens = x.numel() // (h * W) if h * W else 0
-    a = L.GdrNormArgs(tokens, h, W, z_row, _io_of(x), 0, eps, _ptr(x), _ptr(z),
-                      _ptr(_dense(weight)), _ptr(_own("out", out)))
-    L.check(L.lib().gdr_gated_rmsnorm_fwd(ctypes.byref(a), _stream(None, x.device)),
-            "gdr_gated_rmsnorm_fwd")
+    weight = _dense(weight)
+    L.check(L.packed("gdr_gated_rmsnorm_fwd")(
+        L.GDR_NORM(tokens, h, W, z_row, _io_of(x), 0, eps, x.data_ptr(), _at(z), _at(weight),
+                   _own("out", out).data_ptr()), _raw_stream(out)), "gdr_gated_rmsnorm_fwd")
     return out if sg is None else _home(sg, (host_out,), (out,))[0]
 
 
@@ -687,11 +705,11 @@ def ssm_conv1d_packed_fwd(x, w, bias=None, state=None, *, cu_seqlens, slots=None
         dev = x.device
     x, x_row = _rows(x, 1, 16)
     u = torch.empty((T, C), dtype=x.dtype, device=dev) if u is None else _own("u", u)
-    a = L.ConvPackedArgs(T, C, W, n, rows, x_row, _io_of(x), L.SSM_CONV_SILU if silu else 0,
-                         _ptr(x), _ptr(_dense(w)), _ptr(_dense(bias)), _ptr(state),
-                         _ptr(_dense(cu_seqlens)), _ptr(_dense(slots)), _ptr(u))
-    L.check(L.lib().ssm_conv1d_packed_fwd(ctypes.byref(a), _stream(None, dev)),
-            "ssm_conv1d_packed_fwd")
+    w, bias, cu_seqlens, slots = _dense(w), _dense(bias), _dense(cu_seqlens), _dense(slots)
+    L.check(L.packed("ssm_conv1d_packed_fwd")(
+        L.CONV_PACKED(T, C, W, n, rows, x_row, _io_of(x), L.SSM_CONV_SILU if silu else 0,
+                      x.data_ptr(), w.data_ptr(), _at(bias), _at(state), cu_seqlens.data_ptr(),
+                      _at(slots), u.data_ptr()), _raw_stream(u)), "ssm_conv1d_packed_fwd")
     if sg is None:
         return u, state
     if state is None:
