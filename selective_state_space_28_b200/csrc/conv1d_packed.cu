@@ -28,7 +28,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 128, kBatch = 8, kStages = 3;
+constexpr int kThreads = 128, kStages = 3;
 constexpr int kLong = 64, kShort = 8;  // tokens a run
 
 template <typename T, int V> struct Vec {  // V = 1
@@ -139,18 +139,39 @@ template <int BYTES> __device__ __forceinline__ void cp_async(void *dst, const v
 }
 
 template <typename T, int V, int W, int RUN, bool SILU>
-__global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPackedParams p) {
+__global__ void __launch_bounds__(kThreads, RUN == kShort ? 8 : 1) conv1d_packed_kernel(const ConvPackedParams p) {
   using Vc = Vec<T, V>;
   using Raw = typename Vc::Raw;
   constexpr int B = W - 1;  // inputs before a token
   constexpr bool kAhead = RUN == kLong && V > 1;
+  constexpr int kBatch = RUN == kLong ? 8 : 2;  // tokens loaded together
   __shared__ Raw stage[kAhead ? kStages : 1][kAhead ? kBatch : 1][kAhead ? kThreads : 1];
   const int tid = threadIdx.x;
   const int64_t run = (int64_t)blockIdx.y + (int64_t)blockIdx.z * 65535;
   if (run >= p.tokens / RUN + p.nseq) return;
-  const int64_t seq = find_sequence<RUN>(p, run);
   const int64_t c = ((int64_t)blockIdx.x * kThreads + tid) * V;
-  if (c >= p.Cc) return;
+  const bool mine = c < p.Cc;
+  // Channel pairs (each lane of a pair is exactly the scalar fmaf / multiply);
+  // V = 1 leaves the second lane unused.
+  constexpr int VP = (V + 1) / 2;
+  f2 w[VP][W], bias[VP], hist[B > 0 ? B : 1][VP];  // hist: oldest first
+  {
+    float f[V * W];
+    load_floats(p.w + (mine ? c : 0) * W, f);
+#pragma unroll
+    for (int e = 0; e < VP; ++e) {
+#pragma unroll
+      for (int q = 0; q < W; ++q) w[e][q] = mk2(f[2 * e * W + q], V > 1 ? f[((2 * e + 1) % V) * W + q] : 0.f);
+      bias[e] = p.bias ? mk2(__ldg(p.bias + (mine ? c : 0) + 2 * e), V > 1 ? __ldg(p.bias + (mine ? c : 0) + 2 * e + 1) : 0.f)
+                       : mk2(0.f, 0.f);
+    }
+  }
+  auto pairs = [](const float(&f)[V], f2(&h)[VP]) {
+#pragma unroll
+    for (int e = 0; e < VP; ++e) h[e] = mk2(f[2 * e], V > 1 ? f[(2 * e + 1) % V] : 0.f);
+  };
+  const int64_t seq = find_sequence<RUN>(p, run);
+  if (!mine) return;
   const int64_t begin = p.cu[seq], end = p.cu[seq + 1];
   const int64_t j = run - (begin / RUN + seq);
   if (begin < 0 || end < begin || end > p.tokens || j < 0) return;
@@ -175,25 +196,6 @@ __global__ void __launch_bounds__(kThreads) conv1d_packed_kernel(const ConvPacke
     for (int k = 0; k < kStages - 1; ++k) issue(k);
   }
 
-  // Channel pairs (each lane of a pair is exactly the scalar fmaf / multiply);
-  // V = 1 leaves the second lane unused.
-  constexpr int VP = (V + 1) / 2;
-  f2 w[VP][W], bias[VP], hist[B > 0 ? B : 1][VP];  // hist: oldest first
-  {
-    float f[V * W];
-    load_floats(p.w + c * W, f);
-#pragma unroll
-    for (int e = 0; e < VP; ++e) {
-#pragma unroll
-      for (int q = 0; q < W; ++q) w[e][q] = mk2(f[2 * e * W + q], V > 1 ? f[((2 * e + 1) % V) * W + q] : 0.f);
-      bias[e] = p.bias ? mk2(__ldg(p.bias + c + 2 * e), V > 1 ? __ldg(p.bias + c + 2 * e + 1) : 0.f)
-                       : mk2(0.f, 0.f);
-    }
-  }
-  auto pairs = [](const float(&f)[V], f2(&h)[VP]) {
-#pragma unroll
-    for (int e = 0; e < VP; ++e) h[e] = mk2(f[2 * e], V > 1 ? f[(2 * e + 1) % V] : 0.f);
-  };
   if constexpr (B > 0) {
     if (j > 0) {
 #pragma unroll

@@ -144,10 +144,10 @@ cudaError_t run_io(const HeadNormParams &p, cudaStream_t s) {
   constexpr int N = V16<T>::N;
   if (p.width % N == 0 && p.z_row % N == 0) {
     const int64_t nv = p.width / N;
-    if (nv <= 8) return run_vec<T, 8, 1, 2>(p, s);
-    if (nv <= 16) return run_vec<T, 16, 1, 2>(p, s);
-    if (nv <= 32) return run_vec<T, 32, 1, 2>(p, s);
-    if (nv <= 64) return run_vec<T, 32, 2, 2>(p, s);
+    if (nv <= 8) return run_vec<T, 8, 1, 1>(p, s);
+    if (nv <= 16) return run_vec<T, 16, 1, 1>(p, s);
+    if (nv <= 32) return run_vec<T, 32, 1, 1>(p, s);
+    if (nv <= 64) return run_vec<T, 32, 2, 1>(p, s);
     if (nv <= 128) return run_vec<T, 32, 4, 1>(p, s);
   }
   const int64_t blocks = (p.tokens * p.heads + kThreads / 32 - 1) / (kThreads / 32);
