@@ -42,6 +42,8 @@
 // value stays below 2^15 and one 2^-18 of it still has 22 bits.  A warp's
 // lanes that are not finite do not count toward the maxima.
 //
+// Few long sequences are cut into segments (segments_of).
+//
 // Every wait is bounded; one that runs out sets the status word, its warp
 // waits no more, the others' waits run out in turn, and the CTA frees its TMEM.
 #include <cuda_fp16.h>
@@ -87,6 +89,11 @@ struct GdrTcParams {
   uint8_t *rec;   // [slot][head]
   uint8_t *keys;  // [slot][key head][slab]
   int *status;
+  // A sequence cut into segments (see segments_of): how many, which pass, and
+  // the states entering segments 1 .. and the maps of segments 1 .. nseg - 2,
+  // [segment][sequence][head][key side first].
+  int nseg;
+  float *seg_state, *seg_map;
 };
 
 // The record of chunk 0 of sequence `seq`.  Packed sequences start at
@@ -740,7 +747,7 @@ struct Waiter {
   }
 };
 
-template <int KD>
+template <int KD, int PASS>
 __global__ void __launch_bounds__(kThreads, 1)
     gdr_tc_kernel(const __grid_constant__ CUtensorMap mQ,
                   const __grid_constant__ CUtensorMap mV, const __grid_constant__ CUtensorMap mY,
@@ -753,28 +760,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem &s = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const GdrParams &p = tp.p;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t vt = blockIdx.x % tp.vtiles, unit = blockIdx.x / tp.vtiles;
+  // the CTA's sequence, head, segment and value columns
+  const int64_t per = PASS == 0 ? tp.vtiles
+                      : PASS == 1 ? tp.vtiles + (tp.nseg - 2) * (tp.vtiles + 1)
+                                     : (tp.nseg - 1) * tp.vtiles;
+  const int64_t unit = blockIdx.x / per;
+  int64_t vt = blockIdx.x % per;
+  int seg = 0;
+  bool map = false;  // the segment's map: from the identity, without values
+  if (PASS == 2) {
+    seg = 1 + (int)(vt / tp.vtiles);
+    vt %= tp.vtiles;
+  } else if (PASS == 1 && vt >= tp.vtiles) {
+    vt -= tp.vtiles;
+    seg = 1 + (int)(vt / (tp.vtiles + 1));
+    vt %= tp.vtiles + 1;
+    map = vt == tp.vtiles;
+    if (map) vt = 0;
+  }
+  const bool outs = PASS != 1 || seg == 0;  // y is wanted
   const int64_t hd = unit % p.H, seq = unit / p.H;
   int64_t slot, t0, len;
   if (!gdr_sequence(p, seq, slot, t0, len)) return;
   const int64_t g = hd / (p.H / p.Hk);
+  int64_t slot0 = first_slot(tp, seq, t0);
+  if (PASS) {
+    const int64_t all = (len + kC - 1) / kC, c0 = all * seg / tp.nseg, c1 = all * (seg + 1) / tp.nseg;
+    slot0 += c0;
+    t0 += c0 * kC;
+    len = (c1 * kC < len ? c1 * kC : len) - c0 * kC;
+  }
   const int nch = (int)((len + kC - 1) / kC);
   const int64_t v0 = vt * kV;
-  const int64_t so = (slot * p.H + hd) * p.K * p.V + v0;  // the state's first value column
+  const int64_t cols = map ? p.K : p.V;
+  // where the state comes from and goes to: its first value column here
+  const int64_t per_seg = p.nseq * p.H * p.K;
+  const float *src = p.h0 ? p.h0 + (slot * p.H + hd) * p.K * p.V + v0 : nullptr;
+  float *dst = p.h_last ? p.h_last + (slot * p.H + hd) * p.K * p.V + v0 : nullptr;
+  if (PASS == 1) {
+    if (seg > 0) src = nullptr;
+    dst = map ? tp.seg_map + ((seg - 1) * per_seg + unit * p.K) * p.K
+              : tp.seg_state + (seg * per_seg + unit * p.K) * p.V + v0;
+  } else if (PASS == 2) {
+    src = tp.seg_state + ((seg - 1) * per_seg + unit * p.K) * p.V + v0;
+    if (seg < tp.nseg - 1) dst = nullptr;
+  }
 
   // Chain and output warps: value column cv of the tile; chain: half ch.
   const int quarter = warp & 3, ch = warp >> 2;
   const int cv = 32 * quarter + lane;
-  const bool live = v0 + cv < p.V;
+  const bool live = v0 + cv < cols;
   const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
   const float kNorm = KD == 128 ? 11.32f : 8.f;  // sqrt(KD): |S^T k| <= |k| sqrt(KD) max |S|
+  auto start = [&](int r) {  // the state's row r of this lane's column
+    if (!live || r >= p.K) return 0.f;
+    return map ? (r == cv ? 1.f : 0.f) : src ? src[(int64_t)r * p.V + cv] : 0.f;
+  };
 
-  if (nch == 0) {  // an empty sequence hands its state on
-    if (warp < 8 && p.h_last && live) {
-      for (int r = ch; r < p.K; r += 2) {
-        const int64_t at = so + (int64_t)r * p.V + cv;
-        p.h_last[at] = p.h0 ? p.h0[at] : 0.f;
-      }
+  if (nch == 0) {  // an empty sequence or segment hands its state on
+    if (PASS) pdl_wait();  // (and no later kernel runs ahead of an earlier one)
+    if (warp < 8 && dst && live) {
+      for (int r = ch; r < p.K; r += 2) dst[(int64_t)r * cols + cv] = start(r);
     }
     return;
   }
@@ -816,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 16 && lane == 0) {
       // ---------------------------------------------------------- keys and queries
       tma_prefetch_desc(&mQ);
-      const uint8_t *keys = tp.keys + (first_slot(tp, seq, t0) * p.Hk + g) * (int64_t)(NP * kSlab);
+      const uint8_t *keys = tp.keys + (slot0 * p.Hk + g) * (int64_t)(NP * kSlab);
       pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
@@ -834,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = c > 3 ? c - 3 : 0; i < c; ++i) mbar_wait(&s.fullk[i % 3], (i / 3) & 1, kWaitLimit);
     } else if (warp == 18 && lane == 0) {
       // ---------------------------------------------------------- records
-      const uint8_t *rec = tp.rec + (first_slot(tp, seq, t0) * p.H + hd) * (int64_t)sizeof(Rec);
+      const uint8_t *rec = tp.rec + (slot0 * p.H + hd) * (int64_t)sizeof(Rec);
       pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
@@ -919,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (x == 2 ? tl : th) + 2 * kk, id64, x + kk > 0);
         }
         commit(&s.udone, ph);
-        if (leader) {
+        if (leader && outs) {
 #pragma unroll
           for (int kk = 0; kk < KS16; ++kk)
             mma_ts(ycol, tb + kColS + rcol(kk), dq + koff(kk), id64, kk > 0);
@@ -937,9 +983,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ts(tb + kColS, tb + kColU2 + rcol(kk) + 16 * x, dm + kk * 128, idS, x + kk > 0);
           mma_commit(&s.supdone);
           mma_commit(&s.empty[c % 3]);
+          if (outs) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(ycol, tb + kColR + rcol(kk), dp + 2 * kk, id64, 1);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(ycol, tb + kColR + rcol(kk), dp + 2 * kk, id64, 1);
+          }
         }
         commit(&s.pudone, ph);
       }
@@ -966,6 +1014,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 2; ++e) yf[lane + 32 * e] = rc.cq[lane + 32 * e] * s.ysc[c % 3][quarter];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.rfree[c % 3]);
+      if (!outs) {
+        if (lane == 0) mbar_arrive(&s.yfree[par]);
+        continue;
+      }
       // a whole chunk leaves by TMA (columns behind V are not written), the
       // last one's rows one by one
       const bool whole = nv == kC;
@@ -1061,7 +1113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (8 * i + (lane >> 2) < left && x < __uint_as_float(0x7f800000u)) mx = fmaxf(mx, x);
             }
         }
-        mx = warp_max(mx);
+        mx = map ? 0.f : warp_max(mx);
         // From m, the largest value of the state entering the chunk, bounds of the
         // state and U' leaving it, z + w m = n, and from such an n of the chunk
         // before, bounds of this chunk's R and U, x + y n.  With keys of length at
@@ -1083,12 +1135,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------ the chain
     reg_alloc<kRegChain>();
+    if (PASS == 2) pdl_wait();  // the states entering the segments
     f2 st[KH / 2];  // the half row of this lane, scaled by 2^eS
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < KH; ++i) {
       const int r = ch * KH + i;
-      const float x = p.h0 && live && r < p.K ? p.h0[so + (int64_t)r * p.V + cv] : 0.f;
+      const float x = start(r);
       if (i & 1) st[i / 2].y = x; else st[i / 2].x = x;
       m = fmaxf(m, fabsf(x));
     }
@@ -1129,10 +1182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int q = 0; q < 16; ++q)
         vv[q] = (uint32_t)vp[2 * q * kV] | ((uint32_t)vp[(2 * q + 1) * kV] << 16);
-      if (left < 32) {  // rows behind the end may hold anything
+      if (left < 32 || map) {  // rows behind the end may hold anything
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          if (2 * q >= left) vv[q] = 0u;
+          if (map || 2 * q >= left) vv[q] = 0u;
           else if (2 * q + 1 >= left) vv[q] &= 0xffffu;
         }
       }
@@ -1257,12 +1310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       m = warp_max(m);
       if (lane == 0) s.smax[quarter][ch] = m;
     }
-    if (p.h_last && live && !wait.dead) {
+    if (dst && live && !wait.dead) {
       const float un = pow2i(-eS);
 #pragma unroll
       for (int i = 0; i < KH; ++i) {
         const int r = ch * KH + i;
-        if (r < p.K) p.h_last[so + (int64_t)r * p.V + cv] = un * ((i & 1) ? st[i / 2].y : st[i / 2].x);
+        if (r < p.K) dst[(int64_t)r * cols + cv] = un * ((i & 1) ? st[i / 2].y : st[i / 2].x);
       }
     }
   }
@@ -1271,6 +1324,124 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 17) tmem_dealloc(tb, kTmemCols);
+}
+
+// ---------------------------------------------------------------- segments
+// The state entering segment i + 1 from the one entering segment i: S <- M S +
+// N, N the segment's own state from zeros (in the place of the result), M its
+// map.  One CTA per (sequence, head, 16 value columns), over the segments in
+// turn, a warp 16 key rows; the products as float32 on mma.  A lane takes four
+// neighbouring columns of M for the four k of two steps (the sum's order is
+// free), so M comes in 16-byte loads, the next segment's under this one's.
+constexpr int kCarryCols = 16, kCarryRow = 18;  // (18: no bank conflicts)
+__global__ void __launch_bounds__(256) gdr_carry_kernel(const GdrTcParams tp) {
+  __shared__ __align__(16) float S[2][128][kCarryRow];
+  const GdrParams &p = tp.p;
+  const int K = (int)p.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, t = lane & 3;
+  const int64_t tiles = (p.V + kCarryCols - 1) / kCarryCols;
+  const int64_t unit = blockIdx.x / tiles, v0 = (blockIdx.x % tiles) * kCarryCols;
+  const int64_t per_seg = p.nseq * p.H * p.K;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int k0 = 16 * warp + r;  // rows k0 and k0 + 8, columns v0 + 2 t (+ 8) and the next
+  float *at = tp.seg_state + unit * p.K * p.V + v0;
+  const float *m = tp.seg_map + unit * p.K * p.K;
+  float4 a[8][2];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = k0 + 8 * e, col = 16 * b + 4 * t;  // (K is a multiple of 8)
+        a[b][e] = row < K && col < K ? *reinterpret_cast<const float4 *>(m + (int64_t)row * K + col)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    m += per_seg * p.K;
+  };
+  float c[2][4];
+  auto get = [&](float (&c)[2][4]) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = k0 + 8 * (e >> 1), col = 8 * n + 2 * t + (e & 1);
+        c[n][e] = row < K && v0 + col < p.V ? at[(int64_t)row * p.V + col] : 0.f;
+      }
+  };
+  fetch();
+  get(c);
+  for (int i = 1; i < tp.nseg - 1; ++i) {
+    float(*buf)[kCarryRow] = S[i & 1];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float2 *>(&buf[k0 + 8 * e][8 * n + 2 * t]) = make_float2(c[n][2 * e], c[n][2 * e + 1]);
+    at += per_seg * p.V;
+    float4 w[8][2];
+#pragma unroll
+    for (int b = 0; b < 8; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) w[b][e] = a[b][e];
+    if (i + 1 < tp.nseg - 1) fetch();
+    get(c);  // N
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      if (16 * b >= K) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // k of this step: 16 b + 4 t + 2 h and the next
+        uint32_t ah[4], al[4];
+        split_tf32(h ? w[b][0].z : w[b][0].x, ah[0], al[0]);
+        split_tf32(h ? w[b][1].z : w[b][1].x, ah[1], al[1]);
+        split_tf32(h ? w[b][0].w : w[b][0].y, ah[2], al[2]);
+        split_tf32(h ? w[b][1].w : w[b][1].y, ah[3], al[3]);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint32_t bh[2], bl[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) split_tf32(buf[16 * b + 4 * t + 2 * h + e][8 * n + r], bh[e], bl[e]);
+          mma_tf32(c[n], al, bh);
+          mma_tf32(c[n], ah, bl);
+          mma_tf32(c[n], ah, bh);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = k0 + 8 * (e >> 1), col = 8 * n + 2 * t + (e & 1);
+        if (row < K && v0 + col < p.V) at[(int64_t)row * p.V + col] = c[n][e];
+      }
+  }
+}
+
+// How many segments a sequence is cut into.  Uncut, a call takes its longest
+// sequence's chunks one behind the other, 2.75 us each (K = V = 128), on one SM
+// per head and 128 value columns.  Cut into n >= 3: a first pass runs segment 0,
+// and of segments 1 .. n - 2 the state from zeros and the map of an entering
+// state (the same kernel, from the identity and without values); the carry
+// joins them; a second pass runs segments 1 .. n - 1 from their states.  That
+// is 2 / n of the chunks, about 1.3 us a carry and 10 us of launches, as long
+// as each pass finds an SM for every CTA.  Only for keys of length at most 1,
+// whose maps do not grow.
+int segments_of(const GdrParams &p) {
+  const int64_t vt = (p.V + kV - 1) / kV, base = p.nseq * p.H * vt, sms = device_sm_count();
+  if (!(p.flags & GDR_QK_L2NORM) || base * 3 > sms) return 1;
+  const int64_t chunks = p.rows / kC / p.nseq;
+  int best = 1;
+  double least = 0.9 * 2.75 * (double)chunks;
+  for (int n = 3; n <= 16; ++n) {
+    const int64_t first = p.nseq * p.H * (vt + (n - 2) * (vt + 1));
+    if (first > sms || base * (n - 1) > sms) break;
+    const double t = 2.75 * 2. * (double)((chunks + n - 1) / n) + 1.3 * (n - 2) + 10.;
+    if (t < least) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
 }
 
 bool encode(CUtensorMap *m, const void *ptr, int64_t dim, int64_t heads, int64_t rows, int64_t row,
@@ -1286,22 +1457,37 @@ int64_t slots_of(const GdrParams &p) {
   return p.cu ? p.rows / kC + p.nseq : p.nseq * ((p.L + kC - 1) / kC);
 }
 
+template <int KD, int PASS>
+cudaError_t launch_pass(const GdrTcParams &q, int64_t blocks, const CUtensorMap &mQ, const CUtensorMap &mV,
+                        const CUtensorMap &mY, cudaStream_t s) {
+  const size_t smem = sizeof(GdrSmem<KD>) + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(gdr_tc_kernel<KD, PASS>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(gdr_tc_kernel<KD, PASS>, dim3((unsigned)blocks), dim3(kThreads), smem, s, mQ, mV,
+                          mY, q);
+}
+
 template <int KD>
 cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMap &mQ,
                    const CUtensorMap &mV, const CUtensorMap &mY, cudaStream_t s) {
-  const size_t prep = sizeof(PrepSmem<KD>) + 1024, smem = sizeof(GdrSmem<KD>) + 1024;
+  const size_t prep = sizeof(PrepSmem<KD>) + 1024;
   // (set on every call: the attribute belongs to the current device)
   cudaError_t e = cudaFuncSetAttribute(gdr_prep_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)prep);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(gdr_tc_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t most = 6ll * device_sm_count();
   gdr_prep_kernel<KD><<<(unsigned)(q.units < most ? q.units : most), kPrepThreads, prep, s>>>(mK, mQ, q);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(gdr_tc_kernel<KD>, dim3((unsigned)(q.p.nseq * q.p.H * q.vtiles)),
-                          dim3(kThreads), smem, s, mQ, mV, mY, q);
+  const int64_t units = q.p.nseq * q.p.H;
+  if (q.nseg == 1) return launch_pass<KD, 0>(q, units * q.vtiles, mQ, mV, mY, s);
+  e = launch_pass<KD, 1>(q, units * (q.vtiles + (q.nseg - 2) * (q.vtiles + 1)), mQ, mV, mY, s);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (q.p.V + kCarryCols - 1) / kCarryCols;
+  e = launch_dependent(gdr_carry_kernel, dim3((unsigned)(units * tiles)), dim3(256), 0, s, q);
+  if (e != cudaSuccess) return e;
+  return launch_pass<KD, 2>(q, units * (q.nseg - 1) * q.vtiles, mQ, mV, mY, s);
 }
 
 }  // namespace
@@ -1314,8 +1500,10 @@ bool gdr_tc_supported(const GdrParams &p) {
 }
 
 size_t gdr_tc_workspace(const GdrParams &p) {
+  const size_t nseg = (size_t)segments_of(p);
+  const size_t states = nseg == 1 ? 0 : ((nseg - 1) * p.V + (nseg - 2) * p.K) * (size_t)(p.nseq * p.H * p.K);
   return kGdrStatusBytes + (size_t)(slots_of(p) * p.H) * sizeof(Rec) +
-         (size_t)(slots_of(p) * p.Hk) * (p.K <= 64 ? 1 : 2) * kSlab;
+         (size_t)(slots_of(p) * p.Hk) * (p.K <= 64 ? 1 : 2) * kSlab + states * sizeof(float);
 }
 
 cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
@@ -1327,6 +1515,9 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   q.rec = static_cast<uint8_t *>(workspace) + kGdrStatusBytes;
   q.keys = q.rec + (size_t)(slots_of(p) * p.H) * sizeof(Rec);
   q.status = static_cast<int *>(workspace);
+  q.nseg = segments_of(p);
+  q.seg_state = reinterpret_cast<float *>(q.keys + (size_t)(slots_of(p) * p.Hk) * (p.K <= 64 ? 1 : 2) * kSlab);
+  q.seg_map = q.seg_state + (size_t)(q.nseg - 1) * p.nseq * p.H * p.K * p.V;
   CUtensorMap mK, mQ, mV, mY;
   if (!encode(&mK, p.k, p.K, p.Hk, p.rows, p.k_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !encode(&mQ, p.q, p.K, p.Hk, p.rows, p.q_row, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||

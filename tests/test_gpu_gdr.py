@@ -183,6 +183,47 @@ def test_scan_split_and_carry(cuda_ok, io):
     _close(h, rh, "h_last")
 
 
+@pytest.mark.parametrize("n,L,hk,h,K,V", [(1, 3000, 1, 2, 128, 128), (2, 2049, 1, 1, 64, 96),
+                                          (1, 4111, 1, 1, 128, 200), (3, 1500, 1, 2, 40, 64),
+                                          (1, 2500, 2, 6, 128, 64)])
+def test_scan_few_long(cuda_ok, n, L, hk, h, K, V):
+    """Few long sequences, cut into segments that run side by side."""
+    d = I.gdr_inputs(n, L, hk, h, K, V, io="bf16", seed=L, h0=L % 2 == 0)
+    d["A"] = d["A"] * torch.logspace(-4, 0, h)  # long memories among them
+    y, hl = _scan(_dev(d))
+    ry, rh, _ = _ref(d)
+    _close(y, ry, "y")
+    _close(hl, rh, "h_last")
+
+
+def test_scan_few_long_packed(cuda_ok):
+    """The same, packed: segments of very different lengths, some of them and
+    one sequence empty, states updated in place, one sequence skipped."""
+    lengths, hk, h, K, V = [2500, 1, 0, 130, 700], 1, 1, 128, 64
+    d = I.gdr_inputs(1, sum(lengths), hk, h, K, V, io="bf16", seed=5)
+    g = _dev(d)
+    cache = 0.3 * torch.randn(6, h, K, V, device="cuda")
+    before = cache.clone()
+    slots = torch.tensor([5, 0, 2, 1, -1], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+    y = torch.full((1, sum(lengths), h, V), 7.0, dtype=torch.bfloat16, device="cuda")
+    g["h0"] = cache
+    for _ in range(2):
+        cache.copy_(before)
+        _scan(g, cu_seqlens=cu, slots=slots, h_last=cache, y=y)
+    for i, (slot, length) in enumerate(zip(slots.tolist(), lengths)):
+        if slot < 0 or length == 0:
+            continue
+        s = slice(sum(lengths[:i]), sum(lengths[:i + 1]))
+        part = {x: d[x][:, s] for x in ("q", "k", "v", "dt", "beta")}
+        ry, rh, _ = O.gdr_scan(part["q"], part["k"], part["v"], part["dt"], d["A"], part["beta"], d["dt_bias"],
+                               before[slot][None], scale=K ** -0.5)
+        _close(y[:, s], ry, "y %d" % i)
+        _close(cache[slot][None], rh, "state %d" % i)
+    assert torch.equal(cache[[2, 3, 4]], before[[2, 3, 4]])
+    assert (y[:, sum(lengths[:4]):] == 7).all()
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("K,V", [(128, 128), (64, 96), (48, 20)])
 def test_scan_packed_slots(cuda_ok, K, V, io):
