@@ -222,8 +222,16 @@ __global__ void __launch_bounds__(kThreads) gdr_recurrent_kernel(const GdrParams
   const T *kb = static_cast<const T *>(p.k) + g * p.K;
   const T *qb = static_cast<const T *>(p.q) + g * p.K;
   const T *vb = static_cast<const T *>(p.v) + hd * p.V + v0;
+  // a warp's two tokens' gates: lanes 0 and 1
+  const float Ah = p.dt ? p.A[hd] : 0.f, bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
+  T pdt = T(0.f), pbe = T(0.f);
   T pre[kPre], prev[kTok * kCols / kThreads];
   auto fetch = [&](int64_t t) {
+    if (lane < 2 && t + 2 * warp + lane < len) {
+      const int64_t row = t0 + t + 2 * warp + lane;
+      if (p.dt) pdt = static_cast<const T *>(p.dt)[row * p.dt_row + hd];
+      pbe = static_cast<const T *>(p.beta)[row * p.beta_row + hd];
+    }
 #pragma unroll
     for (int i = 0; i < kPre; ++i) {
       const int idx = tid + kThreads * i;
@@ -253,39 +261,48 @@ __global__ void __launch_bounds__(kThreads) gdr_recurrent_kernel(const GdrParams
       const int idx = tid + kThreads * i;
       vs[idx / kCols][idx % kCols] = ld(&prev[i]);
     }
+    const float dt = ld(&pdt), be = ld(&pbe);
     __syncthreads();
     if (t + kTok < len) fetch(t + kTok);
-    // the token's scalars, two tokens a warp
+    // the tokens' scalars, two tokens a warp
+    static_assert(kTok == 2 * (kThreads / 32), "two tokens a warp");
+    float dot[2][3];
 #pragma unroll
-    for (int i = 0; i < kTok / 8; ++i) {
-      const int tok = warp * (kTok / 8) + i;
+    for (int i = 0; i < 2; ++i) {
       float kk = 0.f, qq = 0.f, qk = 0.f;
 #pragma unroll
       for (int c = 0; c < J; ++c) {
-        const float x = kq[tok][0][lane + 32 * c], y = kq[tok][1][lane + 32 * c];
+        const float x = kq[2 * warp + i][0][lane + 32 * c], y = kq[2 * warp + i][1][lane + 32 * c];
         kk = fmaf(x, x, kk);
         qq = fmaf(y, y, qq);
         qk = fmaf(x, y, qk);
       }
+      dot[i][0] = kk;
+      dot[i][1] = qq;
+      dot[i][2] = qk;
+    }
 #pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        kk += __shfl_xor_sync(0xffffffffu, kk, off);
-        qq += __shfl_xor_sync(0xffffffffu, qq, off);
-        qk += __shfl_xor_sync(0xffffffffu, qk, off);
-      }
-      if (lane == 0 && tok < n) {
-        const int64_t row = t0 + t + tok;
-        const float am1 = expm1f(gdr_log_decay<T>(p, row, hd)), a = 1.f + am1;
-        const float nk = gdr_norm_factor(p, kk), nq = p.scale * gdr_norm_factor(p, qq);
-        sc[tok][0] = am1;
-        sc[tok][1] = gdr_beta<T>(p, row, hd) * nk;
-        sc[tok][2] = a * nk;
-        sc[tok][3] = nq * a;
-        sc[tok][4] = nq * qk;
-      }
+    for (int off = 16; off; off >>= 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 3; ++e) dot[i][e] += __shfl_xor_sync(0xffffffffu, dot[i][e], off);
+    if (lane < 2) {
+      float d = dt + bias;
+      if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
+      const float am1 = p.dt ? expm1f(d * Ah) : 0.f, a = 1.f + am1;
+      const float beta = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be * kLog2e)) : be;
+      const float nk = gdr_norm_factor(p, lane ? dot[1][0] : dot[0][0]);
+      const float nq = p.scale * gdr_norm_factor(p, lane ? dot[1][1] : dot[0][1]);
+      float *o = sc[2 * warp + lane];
+      o[0] = am1;
+      o[1] = beta * nk;
+      o[2] = a * nk;
+      o[3] = nq * a;
+      o[4] = nq * (lane ? dot[1][2] : dot[0][2]);
     }
     __syncthreads();
-    for (int tok = 0; tok < n; ++tok) {
+    auto token = [&](int tok) {
       const float4 *k4 = reinterpret_cast<const float4 *>(kq[tok][0]) + r;
       const float4 *q4 = reinterpret_cast<const float4 *>(kq[tok][1]) + r;
       f2 k2[J][2], ka = mk2(0.f, 0.f), qa = ka, kc = ka, qc = ka;
@@ -316,6 +333,14 @@ __global__ void __launch_bounds__(kThreads) gdr_recurrent_kernel(const GdrParams
         s[j][1] = fma2(k2[j][1], mk2(u, u), fma2(am1, s[j][1], s[j][1]));
       }
       if (r == 0) ys[tok][cl] = fmaf(sc[tok][4], u, sc[tok][3] * qs);
+    };
+    // (whole stages unrolled: the next tokens' operands are read ahead of the
+    // chain through the state)
+    if (n == kTok) {
+#pragma unroll
+      for (int tok = 0; tok < kTok; ++tok) token(tok);
+    } else {
+      for (int tok = 0; tok < n; ++tok) token(tok);
     }
     __syncthreads();
     for (int i = tid; i < n * kCols; i += kThreads) {

@@ -1138,12 +1138,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PASS == 2) pdl_wait();  // the states entering the segments
     f2 st[KH / 2];  // the half row of this lane, scaled by 2^eS
     float m = 0.f;
+    if (src) {  // (loads without branches between them: all in flight together)
+      const float *sp = src + (live ? cv : 0);
+      float x[KH];
 #pragma unroll
-    for (int i = 0; i < KH; ++i) {
-      const int r = ch * KH + i;
-      const float x = start(r);
-      if (i & 1) st[i / 2].y = x; else st[i / 2].x = x;
-      m = fmaxf(m, fabsf(x));
+      for (int i = 0; i < KH; ++i) {
+        const int64_t r = ch * KH + i;
+        x[i] = sp[(r < p.K ? r : 0) * p.V];
+      }
+#pragma unroll
+      for (int i = 0; i < KH; ++i) {
+        if (!live || ch * KH + i >= p.K) x[i] = 0.f;
+        m = fmaxf(m, fabsf(x[i]));
+      }
+#pragma unroll
+      for (int i = 0; i < KH / 2; ++i) st[i] = mk2(x[2 * i], x[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < KH / 2; ++i) st[i] = mk2(start(ch * KH + 2 * i), start(ch * KH + 2 * i + 1));
+      m = map ? 1.f : 0.f;
     }
     m = warp_max(m);
     if (lane == 0) s.smax[quarter][ch] = m;
@@ -1423,7 +1436,7 @@ __global__ void __launch_bounds__(256) gdr_carry_kernel(const GdrTcParams tp) {
 // and of segments 1 .. n - 2 the state from zeros and the map of an entering
 // state (the same kernel, from the identity and without values); the carry
 // joins them; a second pass runs segments 1 .. n - 1 from their states.  That
-// is 2 / n of the chunks, about 1.3 us a carry and 10 us of launches, as long
+// is 2 / n of the chunks, about 1.3 us a carry and 20 us of launches, as long
 // as each pass finds an SM for every CTA.  Only for keys of length at most 1,
 // whose maps do not grow.
 int segments_of(const GdrParams &p) {
@@ -1435,7 +1448,7 @@ int segments_of(const GdrParams &p) {
   for (int n = 3; n <= 16; ++n) {
     const int64_t first = p.nseq * p.H * (vt + (n - 2) * (vt + 1));
     if (first > sms || base * (n - 1) > sms) break;
-    const double t = 2.75 * 2. * (double)((chunks + n - 1) / n) + 1.3 * (n - 2) + 10.;
+    const double t = 2.75 * 2. * (double)((chunks + n - 1) / n) + 1.3 * (n - 2) + 20.;
     if (t < least) {
       least = t;
       best = n;
