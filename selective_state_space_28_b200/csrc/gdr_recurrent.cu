@@ -176,23 +176,26 @@ cudaError_t step_io(const GdrParams &p, cudaStream_t s) {
 }
 
 // ------------------------------------------------------- the prompt, by token
-// One CTA per (32 value columns, head, sequence), the state in registers: a
-// warp owns four columns, eight lanes to a column, each with 4 J of its K
-// rows (float4 groups 8 lanes apart, so a warp's shared-memory reads of k and
-// q are whole 128-byte lines).  Tokens are staged kTok at a time as float32,
-// the next stage's raw values held in registers while this one runs; a
-// token's two products are reduced with three shuffles.  The chain from token
-// to token (products, shuffles, write) bounds it, not bytes or flops.
-constexpr int kTok = 16, kCols = 32;
+// One CTA per (32 value columns, head, sequence).  Warps 0-3 run the chain with
+// the state in registers: eight lanes to a pair of columns, each with 4 J of its
+// K rows (float4 groups 8 lanes apart, so a warp's shared-memory reads of k and
+// q are whole 128-byte lines, and serve two columns); a token's two products
+// are reduced with three shuffles.  Warps 4-7 bring the next TOK tokens to
+// shared memory as float32 and make their scalars, with the ones after in
+// flight, and store the last ones' y.  The chain from token to token (products,
+// shuffles, write) bounds it, not bytes or flops: some 370 cycles a token at K =
+// 128 (one group of warps for both took 620).
+constexpr int kCols = 32, kGroup = 128;
 
-template <typename T, int J>
-__global__ void __launch_bounds__(kThreads) gdr_recurrent_kernel(const GdrParams p) {
+template <typename T, int J, int TOK>
+__global__ void __launch_bounds__(2 * kGroup, 1) gdr_recurrent_kernel(const GdrParams p) {
   constexpr int KP = 32 * J;
-  constexpr int kPre = kTok * 2 * KP / kThreads;
-  __shared__ __align__(16) float kq[kTok][2][KP];
-  __shared__ float vs[kTok][kCols], ys[kTok][kCols];
-  __shared__ float sc[kTok][5];  // a - 1, b nk, a nk, scale nq a, scale nq nk (q . k)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kPre = TOK * 2 * KP / kGroup, kPreV = TOK * kCols / kGroup;
+  constexpr int kPer = TOK / (kGroup / 32);  // tokens whose scalars a warp makes
+  __shared__ __align__(16) float kq[2][TOK][2][KP];
+  __shared__ float vs[2][TOK][kCols], ys[2][TOK][kCols];
+  __shared__ float sc[2][TOK][5];  // a - 1, b nk, a nk, scale nq a, scale nq nk (q . k)
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int64_t vtiles = (p.V + kCols - 1) / kCols;
   const int64_t v0 = (blockIdx.x % vtiles) * kCols;
   const int64_t unit = blockIdx.x / vtiles;
@@ -201,166 +204,201 @@ __global__ void __launch_bounds__(kThreads) gdr_recurrent_kernel(const GdrParams
   if (!gdr_sequence(p, seq, slot, t0, len)) return;
   const int K = (int)p.K;
   const int64_t g = hd / (p.H / p.Hk);
-  const int r = lane & 7;
-  const int cl = warp * 4 + (lane >> 3);  // column of the tile
-  const bool live = v0 + cl < p.V;
-  const int64_t so = (slot * p.H + hd) * p.K * p.V + v0 + cl;
+  const int64_t stages = (len + TOK - 1) / TOK;
 
-  f2 s[J][2];
+  if (threadIdx.x >= kGroup) {
+    // ---------------------------------------------------------- staging
+    const int tid = threadIdx.x - kGroup;
+    const T *kb = static_cast<const T *>(p.k) + g * p.K;
+    const T *qb = static_cast<const T *>(p.q) + g * p.K;
+    const T *vb = static_cast<const T *>(p.v) + hd * p.V + v0;
+    T *yb = static_cast<T *>(p.y) + (t0 * p.H + hd) * p.V + v0;
+    // the gates of a warp's tokens: lanes 0 ..
+    const float Ah = p.dt ? p.A[hd] : 0.f, bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
+    T pdt = T(0.f), pbe = T(0.f), pre[kPre], prev[kPreV];
+    auto fetch = [&](int64_t t) {
+      if (lane < kPer && t + kPer * warp + lane < len) {
+        const int64_t row = t0 + t + kPer * warp + lane;
+        if (p.dt) pdt = static_cast<const T *>(p.dt)[row * p.dt_row + hd];
+        pbe = static_cast<const T *>(p.beta)[row * p.beta_row + hd];
+      }
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
-    float x[4];
+      for (int i = 0; i < kPre; ++i) {
+        const int idx = tid + kGroup * i;
+        const int tok = idx / (2 * KP), w = idx / KP % 2, c = idx % KP;
+        const int64_t row = t0 + t + tok;
+        pre[i] = T(0.f);
+        if (t + tok < len && c < K) pre[i] = w ? qb[row * p.q_row + c] : kb[row * p.k_row + c];
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int row = 32 * j + 4 * r + e;
-      x[e] = p.h0 && live && row < K ? p.h0[so + (int64_t)row * p.V] : 0.f;
+      for (int i = 0; i < kPreV; ++i) {
+        const int idx = tid + kGroup * i;
+        const int tok = idx / kCols, c = idx % kCols;
+        prev[i] = T(0.f);
+        if (t + tok < len && v0 + c < p.V) prev[i] = vb[(t0 + t + tok) * p.v_row + c];
+      }
+    };
+    auto stage = [&](int64_t st) {  // what fetch(st TOK) brought
+      const int b = (int)(st & 1);
+#pragma unroll
+      for (int i = 0; i < kPre; ++i) {
+        const int idx = tid + kGroup * i;
+        kq[b][idx / (2 * KP)][idx / KP % 2][idx % KP] = ld(&pre[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kPreV; ++i) {
+        const int idx = tid + kGroup * i;
+        vs[b][idx / kCols][idx % kCols] = ld(&prev[i]);
+      }
+      const float dt = ld(&pdt), be = ld(&pbe);
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (st + 1 < stages) fetch((st + 1) * TOK);
+      float mine[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        float dot[3] = {0.f, 0.f, 0.f};  // k.k, q.q, q.k
+#pragma unroll
+        for (int c = 0; c < J; ++c) {
+          const float x = kq[b][kPer * warp + i][0][lane + 32 * c];
+          const float y = kq[b][kPer * warp + i][1][lane + 32 * c];
+          dot[0] = fmaf(x, x, dot[0]);
+          dot[1] = fmaf(y, y, dot[1]);
+          dot[2] = fmaf(x, y, dot[2]);
+        }
+#pragma unroll
+        for (int off = 16; off; off >>= 1)
+#pragma unroll
+          for (int e = 0; e < 3; ++e) dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], off);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (lane == i) mine[e] = dot[e];
+      }
+      if (lane < kPer) {
+        float d = dt + bias;
+        if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
+        const float am1 = p.dt ? expm1f(d * Ah) : 0.f, a = 1.f + am1;
+        const float beta = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be * kLog2e)) : be;
+        const float nk = gdr_norm_factor(p, mine[0]), nq = p.scale * gdr_norm_factor(p, mine[1]);
+        float *o = sc[b][kPer * warp + lane];
+        o[0] = am1;
+        o[1] = beta * nk;
+        o[2] = a * nk;
+        o[3] = nq * a;
+        o[4] = nq * mine[2];
+      }
+    };
+    auto output = [&](int64_t st) {
+      const int n = (int)(len - st * TOK < TOK ? len - st * TOK : TOK);
+      if (v0 + lane < p.V) {
+        for (int tok = warp; tok < n; tok += kGroup / 32)
+          st_io(yb + (st * TOK + tok) * p.H * p.V + lane, ys[st & 1][tok][lane]);
+      }
+    };
+    if (stages > 0) {
+      fetch(0);
+      stage(0);
     }
-    s[j][0] = mk2(x[0], x[1]);
-    s[j][1] = mk2(x[2], x[3]);
+    __syncthreads();
+    for (int64_t st = 0; st < stages; ++st) {
+      if (st > 0) output(st - 1);
+      if (st + 1 < stages) stage(st + 1);
+      __syncthreads();
+    }
+    if (stages > 0) output(stages - 1);
+    return;
   }
 
-  const T *kb = static_cast<const T *>(p.k) + g * p.K;
-  const T *qb = static_cast<const T *>(p.q) + g * p.K;
-  const T *vb = static_cast<const T *>(p.v) + hd * p.V + v0;
-  // a warp's two tokens' gates: lanes 0 and 1
-  const float Ah = p.dt ? p.A[hd] : 0.f, bias = p.dt && p.dt_bias ? p.dt_bias[hd] : 0.f;
-  T pdt = T(0.f), pbe = T(0.f);
-  T pre[kPre], prev[kTok * kCols / kThreads];
-  auto fetch = [&](int64_t t) {
-    if (lane < 2 && t + 2 * warp + lane < len) {
-      const int64_t row = t0 + t + 2 * warp + lane;
-      if (p.dt) pdt = static_cast<const T *>(p.dt)[row * p.dt_row + hd];
-      pbe = static_cast<const T *>(p.beta)[row * p.beta_row + hd];
-    }
+  // ------------------------------------------------------------ the chain
+  const int r = lane & 7;
+  const int cl = 2 * (warp * 4 + (lane >> 3));  // columns cl and cl + 1 of the tile
+  const bool live[2] = {v0 + cl < p.V, v0 + cl + 1 < p.V};
+  const int64_t so = (slot * p.H + hd) * p.K * p.V + v0 + cl;
+  f2 s[2][J][2];  // [column]
 #pragma unroll
-    for (int i = 0; i < kPre; ++i) {
-      const int idx = tid + kThreads * i;
-      const int tok = idx / (2 * KP), w = idx / KP % 2, c = idx % KP;
-      const int64_t row = t0 + t + tok;
-      pre[i] = T(0.f);
-      if (t + tok < len && c < K) pre[i] = w ? qb[row * p.q_row + c] : kb[row * p.k_row + c];
-    }
+  for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int i = 0; i < kTok * kCols / kThreads; ++i) {
-      const int idx = tid + kThreads * i;
-      const int tok = idx / kCols, c = idx % kCols;
-      prev[i] = T(0.f);
-      if (t + tok < len && v0 + c < p.V) prev[i] = vb[(t0 + t + tok) * p.v_row + c];
-    }
-  };
-  if (len > 0) fetch(0);
-  for (int64_t t = 0; t < len; t += kTok) {
-    const int n = (int)(len - t < kTok ? len - t : kTok);
+    for (int w = 0; w < 2; ++w) {
+      float x[4];
 #pragma unroll
-    for (int i = 0; i < kPre; ++i) {
-      const int idx = tid + kThreads * i;
-      kq[idx / (2 * KP)][idx / KP % 2][idx % KP] = ld(&pre[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kTok * kCols / kThreads; ++i) {
-      const int idx = tid + kThreads * i;
-      vs[idx / kCols][idx % kCols] = ld(&prev[i]);
-    }
-    const float dt = ld(&pdt), be = ld(&pbe);
-    __syncthreads();
-    if (t + kTok < len) fetch(t + kTok);
-    // the tokens' scalars, two tokens a warp
-    static_assert(kTok == 2 * (kThreads / 32), "two tokens a warp");
-    float dot[2][3];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float kk = 0.f, qq = 0.f, qk = 0.f;
-#pragma unroll
-      for (int c = 0; c < J; ++c) {
-        const float x = kq[2 * warp + i][0][lane + 32 * c], y = kq[2 * warp + i][1][lane + 32 * c];
-        kk = fmaf(x, x, kk);
-        qq = fmaf(y, y, qq);
-        qk = fmaf(x, y, qk);
+      for (int e = 0; e < 4; ++e) {
+        const int row = 32 * j + 4 * r + e;
+        x[e] = p.h0 && live[w] && row < K ? p.h0[so + (int64_t)row * p.V + w] : 0.f;
       }
-      dot[i][0] = kk;
-      dot[i][1] = qq;
-      dot[i][2] = qk;
+      s[w][j][0] = mk2(x[0], x[1]);
+      s[w][j][1] = mk2(x[2], x[3]);
     }
-#pragma unroll
-    for (int off = 16; off; off >>= 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 3; ++e) dot[i][e] += __shfl_xor_sync(0xffffffffu, dot[i][e], off);
-    if (lane < 2) {
-      float d = dt + bias;
-      if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
-      const float am1 = p.dt ? expm1f(d * Ah) : 0.f, a = 1.f + am1;
-      const float beta = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be * kLog2e)) : be;
-      const float nk = gdr_norm_factor(p, lane ? dot[1][0] : dot[0][0]);
-      const float nq = p.scale * gdr_norm_factor(p, lane ? dot[1][1] : dot[0][1]);
-      float *o = sc[2 * warp + lane];
-      o[0] = am1;
-      o[1] = beta * nk;
-      o[2] = a * nk;
-      o[3] = nq * a;
-      o[4] = nq * (lane ? dot[1][2] : dot[0][2]);
-    }
-    __syncthreads();
+  __syncthreads();
+  for (int64_t st = 0; st < stages; ++st) {
+    const int b = (int)(st & 1);
+    const int n = (int)(len - st * TOK < TOK ? len - st * TOK : TOK);
     auto token = [&](int tok) {
-      const float4 *k4 = reinterpret_cast<const float4 *>(kq[tok][0]) + r;
-      const float4 *q4 = reinterpret_cast<const float4 *>(kq[tok][1]) + r;
-      f2 k2[J][2], ka = mk2(0.f, 0.f), qa = ka, kc = ka, qc = ka;
+      const float4 *k4 = reinterpret_cast<const float4 *>(kq[b][tok][0]) + r;
+      const float4 *q4 = reinterpret_cast<const float4 *>(kq[b][tok][1]) + r;
+      const float *c = sc[b][tok];
+      const f2 zero = mk2(0.f, 0.f);
+      f2 k2[J][2], ka[2] = {zero, zero}, qa[2] = {zero, zero}, kc[2] = {zero, zero}, qc[2] = {zero, zero};
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const float4 kv = k4[8 * j], qv = q4[8 * j];
         k2[j][0] = mk2(kv.x, kv.y);
         k2[j][1] = mk2(kv.z, kv.w);
-        ka = fma2(k2[j][0], s[j][0], ka);
-        kc = fma2(k2[j][1], s[j][1], kc);
-        qa = fma2(mk2(qv.x, qv.y), s[j][0], qa);
-        qc = fma2(mk2(qv.z, qv.w), s[j][1], qc);
-      }
-      ka = add2(ka, kc);
-      qa = add2(qa, qc);
-      float ks = ka.x + ka.y, qs = qa.x + qa.y;
 #pragma unroll
-      for (int off = 1; off < 8; off <<= 1) {
-        ks += __shfl_xor_sync(0xffffffffu, ks, off);
-        qs += __shfl_xor_sync(0xffffffffu, qs, off);
+        for (int w = 0; w < 2; ++w) {
+          ka[w] = fma2(k2[j][0], s[w][j][0], ka[w]);
+          kc[w] = fma2(k2[j][1], s[w][j][1], kc[w]);
+          qa[w] = fma2(mk2(qv.x, qv.y), s[w][j][0], qa[w]);
+          qc[w] = fma2(mk2(qv.z, qv.w), s[w][j][1], qc[w]);
+        }
       }
-      const f2 am1 = mk2(sc[tok][0], sc[tok][0]);
-      // u against the raw key: S <- a S + k_raw u
-      const float u = sc[tok][1] * (vs[tok][cl] - sc[tok][2] * ks);
+      float ks[2], qs[2];
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        s[j][0] = fma2(k2[j][0], mk2(u, u), fma2(am1, s[j][0], s[j][0]));
-        s[j][1] = fma2(k2[j][1], mk2(u, u), fma2(am1, s[j][1], s[j][1]));
+      for (int w = 0; w < 2; ++w) {
+        const f2 x = add2(ka[w], kc[w]), y = add2(qa[w], qc[w]);
+        ks[w] = x.x + x.y;
+        qs[w] = y.x + y.y;
       }
-      if (r == 0) ys[tok][cl] = fmaf(sc[tok][4], u, sc[tok][3] * qs);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          ks[w] += __shfl_xor_sync(0xffffffffu, ks[w], off);
+          qs[w] += __shfl_xor_sync(0xffffffffu, qs[w], off);
+        }
+      const f2 am1 = mk2(c[0], c[0]);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        // u against the raw key: S <- a S + k_raw u
+        const float u = c[1] * (vs[b][tok][cl + w] - c[2] * ks[w]);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          s[w][j][0] = fma2(k2[j][0], mk2(u, u), fma2(am1, s[w][j][0], s[w][j][0]));
+          s[w][j][1] = fma2(k2[j][1], mk2(u, u), fma2(am1, s[w][j][1], s[w][j][1]));
+        }
+        if (r == 0) ys[b][tok][cl + w] = fmaf(c[4], u, c[3] * qs[w]);
+      }
     };
     // (whole stages unrolled: the next tokens' operands are read ahead of the
     // chain through the state)
-    if (n == kTok) {
+    if (n == TOK) {
 #pragma unroll
-      for (int tok = 0; tok < kTok; ++tok) token(tok);
+      for (int tok = 0; tok < TOK; ++tok) token(tok);
     } else {
       for (int tok = 0; tok < n; ++tok) token(tok);
     }
     __syncthreads();
-    for (int i = tid; i < n * kCols; i += kThreads) {
-      const int tok = i / kCols, c = i % kCols;
-      if (v0 + c < p.V)
-        st_io(static_cast<T *>(p.y) + ((t0 + t + tok) * p.H + hd) * p.V + v0 + c, ys[tok][c]);
-    }
-    // (the next stage writes kq, vs and sc, not ys; ys is written again only
-    // after the next two barriers)
   }
-  if (p.h_last && live) {
+  if (p.h_last) {
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const float x[4] = {s[j][0].x, s[j][0].y, s[j][1].x, s[j][1].y};
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 32 * j + 4 * r + e;
-        if (row < K) p.h_last[so + (int64_t)row * p.V] = x[e];
+      for (int w = 0; w < 2; ++w) {
+        const float x[4] = {s[w][j][0].x, s[w][j][0].y, s[w][j][1].x, s[w][j][1].y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 32 * j + 4 * r + e;
+          if (live[w] && row < K) p.h_last[so + (int64_t)row * p.V + w] = x[e];
+        }
       }
-    }
   }
 }
 
@@ -369,10 +407,10 @@ cudaError_t recurrent_io(const GdrParams &p, cudaStream_t s) {
   const int64_t blocks = p.nseq * p.H * ((p.V + kCols - 1) / kCols);
   if (blocks >= (1ll << 31)) return cudaErrorNotSupported;
   const unsigned grid = (unsigned)blocks;
-  if (p.K <= 32) gdr_recurrent_kernel<T, 1><<<grid, kThreads, 0, s>>>(p);
-  else if (p.K <= 64) gdr_recurrent_kernel<T, 2><<<grid, kThreads, 0, s>>>(p);
-  else if (p.K <= 128) gdr_recurrent_kernel<T, 4><<<grid, kThreads, 0, s>>>(p);
-  else gdr_recurrent_kernel<T, 8><<<grid, kThreads, 0, s>>>(p);
+  if (p.K <= 32) gdr_recurrent_kernel<T, 1, 16><<<grid, 2 * kGroup, 0, s>>>(p);
+  else if (p.K <= 64) gdr_recurrent_kernel<T, 2, 16><<<grid, 2 * kGroup, 0, s>>>(p);
+  else if (p.K <= 128) gdr_recurrent_kernel<T, 4, 16><<<grid, 2 * kGroup, 0, s>>>(p);
+  else gdr_recurrent_kernel<T, 8, 8><<<grid, 2 * kGroup, 0, s>>>(p);
   return cudaGetLastError();
 }
 
