@@ -110,15 +110,18 @@ template <int N> __device__ __forceinline__ void store_floats(float *p, const fl
   }
 }
 
-// The last sequence whose first run is not after `run`, by a whole warp: up to
-// 1024 sequences by counting (one round of loads), more by bisection.
+// The sequence with run `run`, by a whole warp: among up to 1024 by looking at
+// all (one round of loads; -1: none), among more by bisection.
 template <int RUN>
 __device__ __forceinline__ int64_t find_sequence(const ConvPackedParams &p, int64_t run) {
   if (p.nseq <= 1024) {
-    int n = 0;
-    for (int i = threadIdx.x & 31; i < (int)p.nseq; i += 32) n += (int64_t)p.cu[i] / RUN + i <= run;
-    n = __reduce_add_sync(0xffffffffu, n);
-    return n > 0 ? n - 1 : 0;
+    int at = -1;
+    for (int i = threadIdx.x & 31; i < (int)p.nseq; i += 32) {
+      const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / RUN + i;
+      if (b < 0 || e <= b || e > p.tokens || first > run || run >= first + (e - b + RUN - 1) / RUN) continue;
+      if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = i;
+    }
+    return __reduce_max_sync(0xffffffffu, at);
   }
   int64_t lo = 0, hi = p.nseq - 1;
   while (lo < hi) {
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, RUN == kShort ? 8 : 1) conv1d_packed
     for (int e = 0; e < VP; ++e) h[e] = mk2(f[2 * e], V > 1 ? f[(2 * e + 1) % V] : 0.f);
   };
   const int64_t seq = find_sequence<RUN>(p, run);
-  if (!mine) return;
+  if (!mine || seq < 0) return;
   const int64_t begin = p.cu[seq], end = p.cu[seq + 1];
   const int64_t j = run - (begin / RUN + seq);
   if (begin < 0 || end < begin || end > p.tokens || j < 0) return;

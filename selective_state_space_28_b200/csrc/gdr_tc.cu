@@ -48,6 +48,8 @@
 // waits no more, the others' waits run out in turn, and the CTA frees its TMEM.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "gdr.cuh"
 #include "internal.h"
@@ -73,7 +75,8 @@ struct Rec {
   // e^g_63; bounds of ek |k| and of T's rows (scaled); T's exponent; the largest
   // write strength, at least 1, of a chunk that contracts the state, or 0
   float gC, ekn, tn, eT, con;
-  float pad[11];
+  float expired;  // a wait ran out
+  float pad[10];
 };
 // and, for a chunk and key head, the keys as scaled float16: KD / 64 slabs of
 // 64 x 64, 128-byte swizzled rows.
@@ -222,6 +225,7 @@ template <int KD> struct __align__(1024) PrepSmem {
   f2 g[kC];  // running sum of log2 of the decays, hi and lo
   float beta[kC], f[kC], h[kC], qq[kC], bv[kC];
   float ekn[2], tn[4];
+  int found[4];
   uint64_t full, done;
   uint32_t taddr;
 };
@@ -294,6 +298,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
   Smem &s = *reinterpret_cast<Smem *>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const GdrParams &p = tp.p;
   const int pt = threadIdx.x, pw = pt >> 5, lane = pt & 31;
+  // (cleared before a CTA of the next kernel can start; what runs out here is
+  // left in the records)
+  if (blockIdx.x == 0 && pt == 0) *tp.status = 0;
+  __threadfence();
   pdl_launch_dependents();
   if (pt == 0) {
     mbar_init(&s.full, 1);
@@ -317,12 +325,19 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
     if (tp.chunks) {
       seq = rs / tp.chunks;
     } else {
-      int before = 0;
-      for (int64_t i0 = 0; i0 < p.nseq; i0 += kPrepThreads) {
-        const int64_t i = i0 + pt;
-        before += __syncthreads_count(i < p.nseq && p.cu[i] / kC + i <= rs);
+      // (looked for among all: bounds that are out of order and sequences that are
+      // skipped leave the others right)
+      int at = -1;
+      for (int64_t i = pt; i < p.nseq; i += kPrepThreads) {
+        const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / kC + i;
+        if (b < 0 || e <= b || e > p.rows || first > rs || rs >= first + (e - b + kC - 1) / kC) continue;
+        if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = (int)i;
       }
-      seq = before > 0 ? before - 1 : 0;
+      at = __reduce_max_sync(0xffffffffu, at);
+      if (lane == 0) s.found[pw] = at;
+      __syncthreads();
+      seq = max(max(s.found[0], s.found[1]), max(s.found[2], s.found[3]));
+      if (seq < 0) continue;
     }
     if (!gdr_sequence(p, seq, slot, t0, len)) continue;
     c = rs - first_slot(tp, seq, t0);
@@ -676,6 +691,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       fac[4 * kC + 2] = tn * sc.x;
       fac[4 * kC + 3] = (float)eT;
       fac[4 * kC + 4] = con;
+      fac[4 * kC + 5] = ok ? 0.f : 1.f;
     }
     fence_async_smem();
     tc_fence_before();
@@ -688,7 +704,6 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
-  if (!ok && tp.status) atomicExch(tp.status, 1);
   if (pt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   __syncthreads();
   if (pw == 1) tmem_dealloc(tb, 64);
@@ -1122,6 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and |U| <= b (|v| + |S|).  Else step by step: |R| <= |v| + |ek k| sqrt(K) m,
         // |U| <= (T's row sums) |R|, |dS| <= sum |k| |U'| <= 128 |U|.
         const float b = rc.con;
+        if (lane == 0 && rc.expired != 0.f) atomicExch(tp.status, 1);
         float4 f = make_float4(65.f * b * b * mx, b, 65.f * b * b * mx, b * kNorm * rc.gC);
         if (!(b > 0.f)) {
           const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn * kNorm;
@@ -1470,12 +1486,25 @@ int64_t slots_of(const GdrParams &p) {
   return p.cu ? p.rows / kC + p.nseq : p.nseq * ((p.L + kC - 1) / kC);
 }
 
+// Lets `kernel` use `bytes` of shared memory: an attribute of the current
+// device, set once for each (setting it costs a microsecond a call).
+template <auto kernel> cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int KD, int PASS>
 cudaError_t launch_pass(const GdrTcParams &q, int64_t blocks, const CUtensorMap &mQ, const CUtensorMap &mV,
                         const CUtensorMap &mY, cudaStream_t s) {
   const size_t smem = sizeof(GdrSmem<KD>) + 1024;
-  const cudaError_t e = cudaFuncSetAttribute(gdr_tc_kernel<KD, PASS>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<gdr_tc_kernel<KD, PASS>>(smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(gdr_tc_kernel<KD, PASS>, dim3((unsigned)blocks), dim3(kThreads), smem, s, mQ, mV,
                           mY, q);
@@ -1485,9 +1514,7 @@ template <int KD>
 cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMap &mQ,
                    const CUtensorMap &mV, const CUtensorMap &mY, cudaStream_t s) {
   const size_t prep = sizeof(PrepSmem<KD>) + 1024;
-  // (set on every call: the attribute belongs to the current device)
-  cudaError_t e = cudaFuncSetAttribute(gdr_prep_kernel<KD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)prep);
+  cudaError_t e = allow_smem<gdr_prep_kernel<KD>>(prep);
   if (e != cudaSuccess) return e;
   const int64_t most = 6ll * device_sm_count();
   gdr_prep_kernel<KD><<<(unsigned)(q.units < most ? q.units : most), kPrepThreads, prep, s>>>(mK, mQ, q);
@@ -1503,11 +1530,25 @@ cudaError_t launch(const GdrTcParams &q, const CUtensorMap &mK, const CUtensorMa
   return launch_pass<KD, 2>(q, units * (q.nseg - 1) * q.vtiles, mQ, mV, mY, s);
 }
 
+// Whether the token-by-token kernel is the faster one: sequences so short that a
+// chunk is mostly padding, and few enough heads.  Measured (K = 128): that one
+// takes 5.5 us and 0.24 us a token for up to 124 CTAs of 32 value columns (L =
+// 16: 8.9 us, L = 64: 20.5), this one 4 us and 13 us for every 148 CTAs of 128
+// (17 us up to L = 64 with 4 heads, 31 us with 256).  Packed sequences may be as
+// long as all rows.
+bool few_tokens(const GdrParams &p) {
+  const int64_t longest = p.cu ? p.rows : p.L, sms = device_sm_count();
+  if (longest > kC) return false;
+  const double ctas = (double)(p.nseq * p.H * ((p.V + 31) / 32));
+  const int64_t waves = (p.nseq * p.H * ((p.V + kV - 1) / kV) + sms - 1) / sms;
+  return (5.5 + 0.24 * (double)longest) * (ctas > 124. ? ctas / 124. : 1.) < 4. + 13. * (double)waves;
+}
+
 }  // namespace
 
 bool gdr_tc_supported(const GdrParams &p) {
   // bf16; whole 16-byte steps for the TMA; 32-bit TMA coordinates
-  return p.io == 1 && p.rows > 0 && p.nseq > 0 && p.K <= 128 && p.K % 8 == 0 && p.V % 8 == 0 &&
+  return p.io == 1 && p.rows > 0 && p.nseq > 0 && !few_tokens(p) && p.K <= 128 && p.K % 8 == 0 && p.V % 8 == 0 &&
          p.q_row % 8 == 0 && p.k_row % 8 == 0 && p.v_row % 8 == 0 && p.rows + kC < (1ll << 31) &&
          p.nseq * p.H * ((p.V + kV - 1) / kV) < (1ll << 31) && slots_of(p) * p.H < (1ll << 31);
 }
@@ -1537,8 +1578,6 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
       !encode(&mV, p.v, p.V, p.H, p.rows, p.v_row, kV, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode(&mY, p.y, p.V, p.H, p.rows, p.H * p.V, 32, CU_TENSOR_MAP_SWIZZLE_NONE, kC / 2))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaMemsetAsync(q.status, 0, sizeof(int), s);
-  if (e != cudaSuccess) return e;
   return p.K <= 64 ? launch<64>(q, mK, mQ, mV, mY, s) : launch<128>(q, mK, mQ, mV, mY, s);
 }
 

@@ -469,15 +469,17 @@ def _rows(t, inner, align):
     return (t, row) if aligned else (t.contiguous(), 0)
 
 
-def _expect(name, t, dtype, shape, device):
-    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device):
+def _expect(name, t, dtype, shape, at):
+    """``at``: index of the device the other tensors are on (-1: the host)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == at):
         return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if tuple(t.shape) != shape:
-        raise ValueError("%s must be %s, got %s" % (name, shape, tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, device))
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.get_device() != at:
+        raise ValueError("%s is on %s, the other tensors on %s" % (
+            name, t.device, "the host" if at < 0 else "cuda:%d" % at))
 
 
 def _own(name, t):
@@ -489,14 +491,18 @@ def _own(name, t):
 
 def _gdr_inputs(q, k, v, dt, A, beta, dt_bias):
     """Checks the tensors a scan and a step share; returns their sizes."""
-    *lead, h, V = v.shape
-    lead, hk, K = tuple(lead), q.shape[-2], q.shape[-1]
-    dev, io = v.device, v.dtype
-    _expect("q", q, io, lead + (hk, K), dev)
-    _expect("k", k, io, lead + (hk, K), dev)
-    _expect("dt", dt, io, lead + (h,), dev)
-    _expect("beta", beta, io, lead + (h,), dev)
+    shape, key, io, dev = v.shape, q.shape, v.dtype, v.get_device()
+    gate, h, V, hk, K = shape[:-1], shape[-2], shape[-1], key[-2], key[-1]
+    # what holds in an ordinary call first, in one line: a small call's host time counts
+    if not (q.dtype is io and k.dtype is io and beta.dtype is io and k.shape == key
+            and key[:-2] == shape[:-2] and beta.shape == gate and q.get_device() == dev
+            and k.get_device() == dev and beta.get_device() == dev):
+        lead = tuple(shape[:-2])
+        _expect("q", q, io, lead + (hk, K), dev)
+        _expect("k", k, io, lead + (hk, K), dev)
+        _expect("beta", beta, io, lead + (h,), dev)
     if dt is not None:
+        _expect("dt", dt, io, gate, dev)
         _expect("A", A, torch.float32, (h,), dev)
         _expect("dt_bias", dt_bias, torch.float32, (h,), dev)
     return hk, K, h, V
@@ -527,7 +533,7 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
         raise ValueError("q, k and v must be [b, L, heads, dim]")
     hk, K, h, V = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
     b, Lq = v.shape[:2]
-    dev = v.device
+    dev = v.get_device()
     n = b
     if cu_seqlens is not None:
         n = cu_seqlens.numel() - 1
@@ -551,7 +557,6 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
         q, k, v, dt, A, beta, dt_bias, h0, cu_seqlens, slots, y = map(
             sg.dev, (q, k, v, dt, A, beta, dt_bias, h0, cu_seqlens, slots, y))
         h_last = h0 if same else sg.dev(h_last)
-        dev = v.device
     q, q_row = _rows(q, 2, 16)
     k, k_row = _rows(k, 2, 16)
     v, v_row = _rows(v, 2, 16)
@@ -559,8 +564,8 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
     beta, beta_row = _rows(beta, 1, beta.element_size())
     if h0 is not None and h0 is not h_last:
         h0 = h0.contiguous()
-    y = torch.empty((b, Lq, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
-    h_last = (torch.empty((n, h, K, V), dtype=torch.float32, device=dev) if h_last is None
+    y = v.new_empty((b, Lq, h, V)) if y is None else _own("y", y)
+    h_last = (v.new_empty((n, h, K, V), dtype=torch.float32) if h_last is None
               else _own("h_last", h_last))
     A, dt_bias = _dense(A), _dense(dt_bias)
     cu_seqlens, slots = _dense(cu_seqlens), _dense(slots)
@@ -571,8 +576,9 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
     nbytes = ctypes.c_size_t(0)
     L.check(L.packed("gdr_chunk_scan_workspace")(L.GDR_SCAN(*fields, 0, 0), ctypes.addressof(nbytes)),
             "gdr_chunk_scan_workspace")
-    if nbytes.value:
-        workspace = _workspace(nbytes.value, workspace, dev)
+    if nbytes.value and (workspace is None
+                         or workspace.numel() * workspace.element_size() < nbytes.value):
+        workspace = v.new_empty(nbytes.value, dtype=torch.uint8)
     st = _raw_stream(y)
     L.check(L.packed("gdr_chunk_scan_fwd")(
         L.GDR_SCAN(*fields, workspace.data_ptr() if nbytes.value else 0, nbytes.value), st),
@@ -610,7 +616,7 @@ def gdr_scan_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, flag
     if v.dim() != 3 or q.dim() != 3:
         raise ValueError("q, k and v must be [b, heads, dim]")
     hk, K, h, V = _gdr_inputs(q, k, v, dt, A, beta, dt_bias)
-    b, dev = v.shape[0], v.device
+    b, dev = v.shape[0], v.get_device()
     rows = state.shape[0] if slots is not None else b
     _expect("slots", slots, torch.int32, (b,), dev)
     _expect("state", _own("state", state), torch.float32, (rows, h, K, V), dev)
@@ -620,13 +626,12 @@ def gdr_scan_step(state, q, k, v, dt, A, beta, dt_bias=None, *, scale=None, flag
         sg = _Staging([v])
         q, k, v, dt, A, beta, dt_bias, state, slots, y = map(
             sg.dev, (q, k, v, dt, A, beta, dt_bias, state, slots, y))
-        dev = v.device
     q, q_row = _rows(q, 2, 16)
     k, k_row = _rows(k, 2, 16)
     v, v_row = _rows(v, 2, 16)
     dt, dt_row = (None, 0) if dt is None else _rows(dt, 1, dt.element_size())
     beta, beta_row = _rows(beta, 1, beta.element_size())
-    y = torch.empty((b, h, V), dtype=v.dtype, device=dev) if y is None else _own("y", y)
+    y = v.new_empty((b, h, V)) if y is None else _own("y", y)
     A, dt_bias, slots = _dense(A), _dense(dt_bias), _dense(slots)
     L.check(L.packed("gdr_scan_step")(
         L.GDR_STEP(b, h, hk, K, V, rows, q_row, k_row, v_row, dt_row, beta_row, _io_of(v), flags,
@@ -648,10 +653,11 @@ def gdr_gated_rmsnorm_fwd(x, z=None, weight=None, eps=1e-5, *, out=None, stream=
             return gdr_gated_rmsnorm_fwd(x, z, weight, eps, out=out)
     if x.dim() < 2:
         raise ValueError("x must be [.., heads, width]")
-    h, W = x.shape[-2:]
-    _expect("z", z, x.dtype, tuple(x.shape), x.device)
-    _expect("weight", weight, torch.float32, (W,), x.device)
-    _expect("out", out, x.dtype, tuple(x.shape), x.device)
+    shape, dev = x.shape, x.get_device()
+    h, W = shape[-2], shape[-1]
+    _expect("z", z, x.dtype, shape, dev)
+    _expect("weight", weight, torch.float32, (W,), dev)
+    _expect("out", out, x.dtype, shape, dev)
     host_out, sg = out, None
     if not x.is_cuda:
         sg = _Staging([x])
@@ -660,7 +666,7 @@ def gdr_gated_rmsnorm_fwd(x, z=None, weight=None, eps=1e-5, *, out=None, stream=
         out = x if same else out
     z, z_row = (None, 0) if z is None else _rows(z if z.dim() > 2 else z[None], 2, 16)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     x = _own("out", out) if x is out else x.contiguous()
     tokens = x.numel() // (h * W) if h * W else 0
     weight = _dense(weight)
@@ -686,7 +692,7 @@ def ssm_conv1d_packed_fwd(x, w, bias=None, state=None, *, cu_seqlens, slots=None
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x must be [T, C] and w [C, W]")
     T, C = x.shape
-    W, n, dev = w.shape[1], cu_seqlens.numel() - 1, x.device
+    W, n, dev = w.shape[1], cu_seqlens.numel() - 1, x.get_device()
     if n < 0:
         raise ValueError("cu_seqlens must have n + 1 entries")
     _expect("w", w, torch.float32, (C, W), dev)
@@ -702,9 +708,8 @@ def ssm_conv1d_packed_fwd(x, w, bias=None, state=None, *, cu_seqlens, slots=None
         sg = _Staging([x])
         x, w, bias, state, cu_seqlens, slots, u = map(
             sg.dev, (x, w, bias, state, cu_seqlens, slots, u))
-        dev = x.device
     x, x_row = _rows(x, 1, 16)
-    u = torch.empty((T, C), dtype=x.dtype, device=dev) if u is None else _own("u", u)
+    u = x.new_empty((T, C)) if u is None else _own("u", u)
     w, bias, cu_seqlens, slots = _dense(w), _dense(bias), _dense(cu_seqlens), _dense(slots)
     L.check(L.packed("ssm_conv1d_packed_fwd")(
         L.CONV_PACKED(T, C, W, n, rows, x_row, _io_of(x), L.SSM_CONV_SILU if silu else 0,

@@ -281,6 +281,30 @@ def test_scan_bad_bounds_are_empty_sequences(cuda_ok):
     assert (cache[1:4] == 0).all() and (cache[0] != 0).any() and (cache[4] != 0).any()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_bounds_out_of_order_leave_the_others(cuda_ok, io):
+    """A sequence of several chunks whose successors' bounds go back is the
+    sequence all the same, in the scan and in the convolution."""
+    n, hk, h, K, V = 500, 1, 1, 64, 64
+    d = I.gdr_inputs(1, n, hk, h, K, V, io=io, seed=14)
+    bounds = [0, 400, 10, 5, 400, 500]
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([3, 0, 1, -1, 2], dtype=torch.int32, device="cuda")  # (5 .. 400 is skipped)
+    cache = torch.zeros(4, h, K, V, device="cuda")
+    g = _dev(d)
+    g["h0"] = cache
+    y, _ = _scan(g, cu_seqlens=cu, slots=slots, h_last=cache)
+    x, w = torch.randn(n, 64), torch.randn(64, 4)
+    u, _ = _ops().ssm_conv1d_packed_fwd(x.cuda(), w.cuda(), cu_seqlens=cu, slots=slots)
+    for a, b, slot in ((0, 400, 3), (400, 500, 2)):
+        part = {k: d[k][:, a:b] for k in ("q", "k", "v", "dt", "beta")}
+        ry, rh, _ = O.gdr_scan(part["q"], part["k"], part["v"], part["dt"], d["A"], part["beta"], d["dt_bias"],
+                               None, scale=K ** -0.5)
+        _close(y[:, a:b], ry, "y")
+        _close(cache[slot][None], rh, "state")
+        _close(u[a:b], O.conv1d_packed(x[a:b], w, None, None, [b - a])[0], "u")
+
+
 def test_scan_no_tokens(cuda_ok):
     d = _dev(I.gdr_inputs(2, 0, 1, 2, 128, 128, seed=1, h0=True))
     y, h = _scan(d)
