@@ -45,9 +45,11 @@ __device__ __forceinline__ float gdr_beta(const GdrParams &p, int64_t row, int64
   return (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-b * kLog2e)) : b;
 }
 
-// 1 / sqrt(|x|^2 + eps) from |x|^2 (1 without the norm).
+// 1 / sqrt(|x|^2 + eps) from |x|^2 (1 without the norm; 0 for a row of zeros,
+// whatever eps).
 __device__ __forceinline__ float gdr_norm_factor(const GdrParams &p, float ss) {
-  return (p.flags & GDR_QK_L2NORM) ? 1.f / sqrtf(ss + p.l2_eps) : 1.f;
+  if (!(p.flags & GDR_QK_L2NORM)) return 1.f;
+  return ss == 0.f ? 0.f : 1.f / sqrtf(ss + p.l2_eps);
 }
 
 }  // namespace ssm

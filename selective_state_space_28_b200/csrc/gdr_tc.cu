@@ -210,6 +210,7 @@ __device__ __forceinline__ float warp_max(float m) {
 
 // ---------------------------------------------------------- what needs no state
 constexpr int kPrepThreads = 128;
+constexpr int kSearched = 1024;  // packed sequences looked through for a record's (more: bisected)
 
 template <int KD> struct __align__(1024) PrepSmem {
   union {
@@ -325,18 +326,28 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
     if (tp.chunks) {
       seq = rs / tp.chunks;
     } else {
-      // (looked for among all: bounds that are out of order and sequences that are
-      // skipped leave the others right)
-      int at = -1;
-      for (int64_t i = pt; i < p.nseq; i += kPrepThreads) {
-        const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / kC + i;
-        if (b < 0 || e <= b || e > p.rows || first > rs || rs >= first + (e - b + kC - 1) / kC) continue;
-        if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = (int)i;
+      if (p.nseq <= kSearched) {
+        // (among all: bounds that are out of order and sequences that are skipped
+        // leave the others right)
+        int at = -1;
+        for (int64_t i = pt; i < p.nseq; i += kPrepThreads) {
+          const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / kC + i;
+          if (b < 0 || e <= b || e > p.rows || first > rs || rs >= first + (e - b + kC - 1) / kC) continue;
+          if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = (int)i;
+        }
+        at = __reduce_max_sync(0xffffffffu, at);
+        if (lane == 0) s.found[pw] = at;
+        __syncthreads();
+        seq = max(max(s.found[0], s.found[1]), max(s.found[2], s.found[3]));
+      } else {
+        int64_t lo = 0, hi = p.nseq - 1;
+        while (lo < hi) {
+          const int64_t mid = (lo + hi + 1) >> 1;
+          if ((int64_t)p.cu[mid] / kC + mid <= rs) lo = mid;
+          else hi = mid - 1;
+        }
+        seq = lo;
       }
-      at = __reduce_max_sync(0xffffffffu, at);
-      if (lane == 0) s.found[pw] = at;
-      __syncthreads();
-      seq = max(max(s.found[0], s.found[1]), max(s.found[2], s.found[3]));
       if (seq < 0) continue;
     }
     if (!gdr_sequence(p, seq, slot, t0, len)) continue;
@@ -384,9 +395,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
           if (p.dt) {
             float d = dtv[e] + bias;
             if (p.flags & SSM_DT_SOFTPLUS) d = softplus(d);
-            l2 = fmaxf(d * Ah * kLog2e, -256.f);
+            l2 = d * Ah * kLog2e;
           }
           b = (p.flags & GDR_BETA_SIGMOID) ? 1.f / (1.f + ex2(-be[e] * kLog2e)) : be[e];
+          if (l2 != l2) b = l2;  // (not a number: seen in everything written)
+          l2 = fmaxf(l2, -256.f);
         }
         gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
         s.beta[2 * lane + e] = b;

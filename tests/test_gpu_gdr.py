@@ -369,6 +369,37 @@ def test_step(cuda_ok, hk, h, K, V, io):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("b,hk,h,K,V", [(80, 16, 32, 64, 64), (130, 10, 20, 128, 128), (300, 8, 8, 32, 96),
+                                        (50, 25, 50, 72, 40), (40, 60, 60, 64, 256)])
+def test_step_large_batch(cuda_ok, b, hk, h, K, V, io):
+    """Enough rows and heads that CTAs stay for several of them: padding among
+    the rows, slices, slots anywhere."""
+    d = I.gdr_inputs(b, 1, hk, h, K, V, io=io, seed=b)
+    g = _dev(d)
+    qkv = torch.cat([g[x][:, 0].flatten(1) for x in ("q", "k", "v")], -1)
+    q, k, v = qkv.split([hk * K, hk * K, h * V], -1)
+    cache = 0.3 * torch.randn(b + 5, h, K, V, device="cuda")
+    before = cache.clone()
+    slots = torch.randperm(b + 5, generator=torch.Generator().manual_seed(b))[:b].to(torch.int32)
+    slots[[1, 2, 7, b - 1]] = -1
+    slots[b // 2] = b + 5
+    live = [i for i in range(b) if 0 <= slots[i] < b + 5]
+    y = torch.full((b, h, V), 7.0, dtype=v.dtype, device="cuda")
+    _ops().gdr_scan_step(cache, q.unflatten(-1, (hk, K)), k.unflatten(-1, (hk, K)), v.unflatten(-1, (h, V)),
+                         g["dt"][:, 0], g["A"], g["beta"][:, 0], dt_bias=g["dt_bias"], slots=slots.cuda(), y=y)
+    at = slots[live].long()
+    sub = {x: d[x][live] for x in ("q", "k", "v", "dt", "beta")}
+    ry, rh, _ = O.gdr_scan(sub["q"], sub["k"], sub["v"], sub["dt"], d["A"], sub["beta"], d["dt_bias"],
+                           before[at.cuda()], scale=K ** -0.5)
+    _close(y[live], ry[:, 0], "y")
+    _close(cache[at.cuda()], rh, "state")
+    dead = [i for i in range(b) if i not in live]
+    assert (y[dead] == 7).all()
+    rest = [i for i in range(b + 5) if i not in at.tolist()]
+    assert torch.equal(cache[rest], before[rest])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_step_slots_padding_slices(cuda_ok, io):
     b, hk, h, K, V = 7, 2, 4, 64, 64
     d = I.gdr_inputs(b, 1, hk, h, K, V, io=io, seed=2)
@@ -581,3 +612,55 @@ def test_host_tensors(cuda_ok):
     u, so = ops.ssm_conv1d_packed_fwd(xc, w, None, st, cu_seqlens=torch.tensor([0, 2, 6], dtype=torch.int32))
     _close(u, ru, "u")
     assert so is st and np.array_equal(_np(st), rs)
+
+
+@pytest.mark.parametrize("io,L", [("f32", 200), ("bf16", 20), ("bf16", 200)])
+def test_scan_not_a_number_stays_in_its_head(cuda_ok, io, L):
+    """A value, key or gate that is not a number is seen in its own sequence and
+    heads from its chunk on, and nowhere else."""
+    for name in ("v", "k", "dt", "beta"):
+        d = I.gdr_inputs(2, L, 2, 4, 64, 64, io=io, seed=3, h0=True)
+        ry, rh, _ = _ref(d)
+        at = L - 5
+        d[name][0, at, 1] = float("nan")
+        heads = [2, 3] if name == "k" else [1]
+        y, h = _scan(_dev(d))
+        assert torch.isnan(h[0, heads]).any() and torch.isnan(y[0, at:, heads]).any(), name
+        ok = [i for i in range(4) if i not in heads]
+        _close(y[:, :, ok], ry[:, :, ok], "y " + name)
+        _close(h[:, ok], rh[:, ok], "state " + name)
+        _close(y[1], ry[1], "the other sequence " + name)
+        _close(y[0, :at // 64 * 64], ry[0, :at // 64 * 64], "chunks before " + name)
+
+
+@pytest.mark.parametrize("io,L", [("f32", 100), ("bf16", 10), ("bf16", 100)])
+def test_zero_rows_without_eps(cuda_ok, io, L):
+    """Rows of zeros have nothing to normalise by, also with l2_eps 0."""
+    d = I.gdr_inputs(1, L, 1, 1, 64, 64, io=io, seed=6, h0=True)
+    d["k"][:, 3:6] = 0
+    d["q"][:, 2:8] = 0
+    y, h = _scan(_dev(d), l2_eps=0.0)
+    ry, rh, _ = _ref(d, l2_eps=1e-30)
+    _close(y, ry, "y")
+    _close(h, rh, "h_last")
+
+
+def test_scan_packed_many(cuda_ok):
+    """More sequences than are put in order or looked through."""
+    g = torch.Generator().manual_seed(1)
+    for n in (300, 1100):
+        lengths = (torch.rand(n, generator=g) * 4).int().tolist()
+        lengths[5], lengths[n - 3] = 150, 70
+        d = I.gdr_inputs(1, sum(lengths), 1, 1, 64, 64, io="bf16", seed=n)
+        cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
+        y, h = _scan(_dev(d), cu_seqlens=cu)
+        for i in (0, 5, 6, n // 2, n - 3, n - 1):
+            s = slice(sum(lengths[:i]), sum(lengths[:i + 1]))
+            if s.stop == s.start:
+                assert (h[i] == 0).all()
+                continue
+            part = {x: d[x][:, s] for x in ("q", "k", "v", "dt", "beta")}
+            ry, rh, _ = O.gdr_scan(part["q"], part["k"], part["v"], part["dt"], d["A"], part["beta"], d["dt_bias"],
+                                   None, scale=8 ** -1.0)
+            _close(y[:, s], ry, "y %d" % i)
+            _close(h[i][None], rh, "state %d" % i)
