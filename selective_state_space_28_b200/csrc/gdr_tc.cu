@@ -88,7 +88,8 @@ struct GdrTcParams {
   GdrParams p;
   int64_t vtiles;
   int64_t chunks;  // of a sequence (dense), or 0: packed
-  int64_t units;   // records
+  int64_t share;   // value heads that the first kernel makes the records of together
+  int64_t units;   // such groups of records
   uint8_t *rec;   // [slot][head]
   uint8_t *keys;  // [slot][key head][slab]
   int *status;
@@ -223,10 +224,10 @@ template <int KD> struct __align__(1024) PrepSmem {
       __align__(16) uint8_t rest[sizeof(Rec) - kRecT];
     };
   };
-  f2 g[kC];  // running sum of log2 of the decays, hi and lo
-  float beta[kC], f[kC], h[kC], qq[kC], bv[kC];
+  f2 g[2][kC];  // running sum of log2 of the decays, hi and lo; a head's and the next's
+  float beta[2][kC], f[kC], h[kC], qq[kC], bv[kC];
   float ekn[2], tn[4];
-  int found[4];
+  int found[2][4];
   uint64_t full, done;
   uint32_t taddr;
 };
@@ -317,11 +318,12 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = s.taddr;
-  uint32_t ph = 0;
+  uint32_t ph = 0, round = 0;
   bool ok = true;
   for (int64_t unit = blockIdx.x; unit < tp.units; unit += gridDim.x) {
     // the sequence and chunk of this record
-    const int64_t hd = unit % p.H, rs = unit / p.H;
+    const int64_t groups = p.H / tp.share, rs = unit / groups, hd0 = unit % groups * tp.share;
+    round ^= 1;
     int64_t seq, c, slot, t0, len;
     if (tp.chunks) {
       seq = rs / tp.chunks;
@@ -336,9 +338,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
           if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = (int)i;
         }
         at = __reduce_max_sync(0xffffffffu, at);
-        if (lane == 0) s.found[pw] = at;
+        if (lane == 0) s.found[round][pw] = at;
         __syncthreads();
-        seq = max(max(s.found[0], s.found[1]), max(s.found[2], s.found[3]));
+        const int(&f)[4] = s.found[round];
+        seq = max(max(f[0], f[1]), max(f[2], f[3]));
       } else {
         int64_t lo = 0, hi = p.nseq - 1;
         while (lo < hi) {
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
     const int64_t left = len - c * kC;
     const int nv = (int)(left < kC ? left : kC);
     t0 += c * kC;
-    const int64_t g = hd / (p.H / p.Hk);
+    const int64_t g = hd0 / (p.H / p.Hk);
 
     if (pt == 0) {
       // (the records before have left the shared memory)
@@ -369,9 +372,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       }
     }
     __syncwarp();
+    // the gates of a head, by the last warp: lane l has tokens 2 l and 2 l + 1
     int64_t g63x = 0;
     float con = 0.f;
-    if (pw == 3) {  // the gates: lane l has tokens 2 l and 2 l + 1
+    auto gates = [&](int64_t hd, int buf) {
       float dtv[2] = {}, be[2] = {};
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
           l2 = fmaxf(l2, -256.f);
         }
         gs[e] = __float2ll_rn(fminf(l2, 256.f) * 17592186044416.f);
-        s.beta[2 * lane + e] = b;
+        s.beta[buf][2 * lane + e] = b;
         fine = fine && l2 <= 0.f && b >= 0.f && b <= 2.f;
         bmax = fmaxf(bmax, b);
       }
@@ -420,9 +424,10 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
         return mk2((float)(int)(g >> 34) * 0.0009765625f,
                    (float)(int)((g & ((1ll << 34) - 1)) >> 10) * 5.8207660913467407e-11f);
       };
-      s.g[2 * lane] = parts(sum - gs[1]);
-      s.g[2 * lane + 1] = parts(sum);
-    }
+      s.g[buf][2 * lane] = parts(sum - gs[1]);
+      s.g[buf][2 * lane + 1] = parts(sum);
+    };
+    if (pw == 3) gates(hd0, 0);
     ok = mbar_wait(&s.full, ph, kWaitLimit) && ok;
     if (pw == 0) {
       if (elect_one()) {
@@ -463,258 +468,272 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
     // of G this row's columns of its own 32-token block; own: of its 16-token block
     const int blk = pw & 1;
     const bool up = lane >= 16;  // the second of the two 16-token blocks
-    uint32_t r0[16], own[16];
-    {
-      uint32_t r1[16];
-      tmem_ld16(grow + 32 * blk, r0);
-      tmem_ld16(grow + 32 * blk + 16, r1);
-      tmem_ld_wait();
+    float n2, f = 0.f, nf = 0.f;
+    for (int hj = 0; hj < tp.share; ++hj) {  // the value heads that share these keys
+      const int64_t hd = hd0 + hj;
+      const int gb = hj & 1;
+      uint32_t r0[16], own[16];
+      {
+        uint32_t r1[16];
+        tmem_ld16(grow + 32 * blk, r0);
+        tmem_ld16(grow + 32 * blk + 16, r1);
+        tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 16; ++q) own[q] = up ? r1[q] : r0[q];
-    }
-    float n2;
-    if (isk) {
-      uint32_t t[8];  // own[lane & 15], bit by bit of the index
-#pragma unroll
-      for (int q = 0; q < 8; ++q) t[q] = lane & 8 ? own[q + 8] : own[q];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) t[q] = lane & 4 ? t[q + 4] : t[q];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) t[q] = lane & 2 ? t[q + 2] : t[q];
-      n2 = __uint_as_float(lane & 1 ? t[1] : t[0]);
-    } else {
-      n2 = s.qq[tok];
-    }
-    // the row's power of two f = 2^-e, |row| f in 1 .. 2; its norm factor beside
-    // rows scaled so
-    int e = ((int)((__float_as_uint(n2) >> 23) & 255u) - 127) >> 1;
-    e = !(n2 > 0.f) ? 0 : e < -60 ? -60 : e > 60 ? 60 : e;
-    float f = 0.f, nf = 0.f;
-    if (on) {
-      f = pow2i(-e);
-      nf = pow2i(e);
-      if (p.flags & GDR_QK_L2NORM) {
-        const float a = n2 + p.l2_eps, r = rsqrtf(a);
-        // (one Newton step on the hardware's; infinite norms give 0)
-        nf = n2 == 0.f || !(r > 0.f) ? 0.f : nf * (r * fmaf(-0.5f * a * r, r, 1.5f));
+        for (int q = 0; q < 16; ++q) own[q] = up ? r1[q] : r0[q];
       }
-      if (n2 != n2) nf = n2;
-    }
-    const f2 gi = s.g[tok], g63 = s.g[63], gend = s.g[tok | 15];
-    const float eg = ex2(gi.x + gi.y);
-    float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, ek) - kRecT));
-    float rowf = f;
-    if (isk) {
-      const float b = s.beta[tok];
-      rowf = nf * nf * b * f;
-      s.bv[tok] = nf * b;
-      fac[0 * kC + tok] = -nf * eg;                              // ek
-      fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
-      s.f[tok] = f;
-      s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
-      const float m = warp_max(2.f * nf * eg);
-      if (lane == 0) s.ekn[pw] = m;
-    } else {
-      fac[2 * kC + tok] = p.scale * nf;  // cq
-      fac[3 * kC + tok] = f * eg;        // fq
-    }
-    __syncthreads();  // f, h
-    if (hd % (p.H / p.Hk) == 0) {  // the keys, scaled; rows behind the end may hold anything
-      uint8_t *out = tp.keys + (rs * p.Hk + g) * (int64_t)(NP * kSlab);
+      if (hj == 0) {
+        if (isk) {
+          uint32_t t[8];  // own[lane & 15], bit by bit of the index
 #pragma unroll
-      for (int i = 0; i < NP * 4; ++i) {
-        const int at = (i & 3) * kPrepThreads + pt;  // 16 bytes of the slab: any swizzle
-        const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[i >> 2][16 * at]);
-        const float fr = s.f[at >> 3];
-        const uint32_t f2x = __byte_perm(__float_as_uint(fr), 0, 0x3232);  // (a power of two: exact)
-        uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          for (int q = 0; q < 8; ++q) t[q] = lane & 8 ? own[q + 8] : own[q];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f2 y = fma_bf16x2(w[e], f2x, mk2(0.f, 0.f));
-          w[e] = (at >> 3) < nv ? pack_h2(y.x, y.y) : 0u;
+          for (int q = 0; q < 4; ++q) t[q] = lane & 4 ? t[q + 4] : t[q];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) t[q] = lane & 2 ? t[q + 2] : t[q];
+          n2 = __uint_as_float(lane & 1 ? t[1] : t[0]);
+        } else {
+          n2 = s.qq[tok];
         }
-        *reinterpret_cast<uint4 *>(out + (i >> 2) * kSlab + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+        // the row's power of two f = 2^-e, |row| f in 1 .. 2; its norm factor beside
+        // rows scaled so
+        int e = ((int)((__float_as_uint(n2) >> 23) & 255u) - 127) >> 1;
+        e = !(n2 > 0.f) ? 0 : e < -60 ? -60 : e > 60 ? 60 : e;
+        if (on) {
+          f = pow2i(-e);
+          nf = pow2i(e);
+          if (p.flags & GDR_QK_L2NORM) {
+            const float a = n2 + p.l2_eps, r = rsqrtf(a);
+            // (one Newton step on the hardware's; infinite norms give 0)
+            nf = n2 == 0.f || !(r > 0.f) ? 0.f : nf * (r * fmaf(-0.5f * a * r, r, 1.5f));
+          }
+          if (n2 != n2) nf = n2;
+        }
       }
-      __syncthreads();  // A and P take the keys' place
-    }
-
-    // A and P, 16 columns at a time.  In the row's own 16-token block the decays
-    // are taken element by element; in blocks before it they go by way of the
-    // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
-    // above 1.
-    uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
-    const bool part = nv < kC;
-    auto put = [&](int J, const f2(&x)[8]) {
-      f2 z[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) z[q] = part && !on ? mk2(0.f, 0.f) : x[q];  // (may hold anything)
+      if (hj > 0) {  // the head's before has left the shared memory
+        if (pt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncthreads();
+      }
+      const f2(&sg)[kC] = s.g[gb];
+      const f2 gi = sg[tok], g63 = sg[63], gend = sg[tok | 15];
+      const float eg = ex2(gi.x + gi.y);
+      float *fac = reinterpret_cast<float *>(s.rest + (offsetof(Rec, ek) - kRecT));
+      float rowf = f;
       if (isk) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
-              make_float4(z[2 * q].x, z[2 * q].y, z[2 * q + 1].x, z[2 * q + 1].y);
+        const float b = s.beta[gb][tok];
+        rowf = nf * nf * b * f;
+        s.bv[tok] = nf * b;
+        fac[0 * kC + tok] = -nf * eg;                              // ek
+        fac[1 * kC + tok] = ex2((g63.x - gi.x) + (g63.y - gi.y));  // cu
+        s.f[tok] = f;
+        s.h[tok] = f * ex2((gend.x - gi.x) + (gend.y - gi.y));
+        const float m = warp_max(2.f * nf * eg);
+        if (lane == 0) s.ekn[pw] = m;
       } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          *reinterpret_cast<uint4 *>(P + sw128(tok, 2 * J + q)) =
-              make_uint4(pack_h2(z[4 * q].x, z[4 * q].y), pack_h2(z[4 * q + 1].x, z[4 * q + 1].y),
-                         pack_h2(z[4 * q + 2].x, z[4 * q + 2].y), pack_h2(z[4 * q + 3].x, z[4 * q + 3].y));
+        fac[2 * kC + tok] = p.scale * nf;  // cq
+        fac[3 * kC + tok] = f * eg;        // fq
       }
-    };
-    auto before = [&](int J, const uint32_t(&r)[16], f2(&x)[8]) {  // a block before the row's own
-      const f2 ge = s.g[16 * J + 15];
-      const float fr = rowf * ex2((gi.x - ge.x) + (gi.y - ge.y));
+      __syncthreads();  // f, h
+      if (hd % (p.H / p.Hk) == 0) {  // the keys, scaled; rows behind the end may hold anything
+        uint8_t *out = tp.keys + (rs * p.Hk + g) * (int64_t)(NP * kSlab);
+#pragma unroll
+        for (int i = 0; i < NP * 4; ++i) {
+          const int at = (i & 3) * kPrepThreads + pt;  // 16 bytes of the slab: any swizzle
+          const uint4 u = *reinterpret_cast<const uint4 *>(&s.kq[i >> 2][16 * at]);
+          const float fr = s.f[at >> 3];
+          const uint32_t f2x = __byte_perm(__float_as_uint(fr), 0, 0x3232);  // (a power of two: exact)
+          uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f2 y = fma_bf16x2(w[e], f2x, mk2(0.f, 0.f));
+            w[e] = (at >> 3) < nv ? pack_h2(y.x, y.y) : 0u;
+          }
+          *reinterpret_cast<uint4 *>(out + (i >> 2) * kSlab + 16 * at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncthreads();  // A and P take the keys' place
+      }
+
+      // A and P, 16 columns at a time.  In the row's own 16-token block the decays
+      // are taken element by element; in blocks before it they go by way of the
+      // block's last token, e^(g_i - g_j) = e^(g_i - g_end) e^(g_end - g_j), no factor
+      // above 1.
+      uint8_t *P = s.rest;  // (16-byte aligned; the copy to a swizzled place keeps the chunk order)
+      const bool part = nv < kC;
+      auto put = [&](int J, const f2(&x)[8]) {
+        f2 z[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) z[q] = part && !on ? mk2(0.f, 0.f) : x[q];  // (may hold anything)
+        if (isk) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4 *>(&s.Am[tok][16 * J + 4 * q]) =
+                make_float4(z[2 * q].x, z[2 * q].y, z[2 * q + 1].x, z[2 * q + 1].y);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            *reinterpret_cast<uint4 *>(P + sw128(tok, 2 * J + q)) =
+                make_uint4(pack_h2(z[4 * q].x, z[4 * q].y), pack_h2(z[4 * q + 1].x, z[4 * q + 1].y),
+                           pack_h2(z[4 * q + 2].x, z[4 * q + 2].y), pack_h2(z[4 * q + 3].x, z[4 * q + 3].y));
+        }
+      };
+      auto before = [&](int J, const uint32_t(&r)[16], f2(&x)[8]) {  // a block before the row's own
+        const f2 ge = sg[16 * J + 15];
+        const float fr = rowf * ex2((gi.x - ge.x) + (gi.y - ge.y));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 h = *reinterpret_cast<const float4 *>(&s.h[16 * J + 4 * q]);
+          x[2 * q] = mul2(mul2(mk2(h.x, h.y), mk2(fr, fr)),
+                          mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])));
+          x[2 * q + 1] = mul2(mul2(mk2(h.z, h.w), mk2(fr, fr)),
+                              mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
+        }
+      };
+      {
+        f2 x[8];
+        float o[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const int j = (tok & ~15) + q;
+          const f2 gj = sg[j];
+          const f2 d = add2(gi, mk2(-gj.x, -gj.y));
+          const bool in = isk ? j < tok : j <= tok;
+          o[q] = in ? __uint_as_float(own[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
+        }
+        before(2 * blk, r0, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = up ? x[q] : mk2(o[2 * q], o[2 * q + 1]);
+        put(2 * blk, x);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = up ? mk2(o[2 * q], o[2 * q + 1]) : mk2(0.f, 0.f);
+        put(2 * blk + 1, x);
+      }
+#pragma unroll 1
+      for (int J = 0; J < 2; ++J) {
+        f2 x[8];
+        if (blk) {
+          tmem_ld16(grow + 16 * J, r0);
+          tmem_ld_wait();
+          before(J, r0, x);
+          put(J, x);
+        } else if (!isk) {  // above P's diagonal blocks
+#pragma unroll
+          for (int q = 0; q < 8; ++q) x[q] = mk2(0.f, 0.f);
+          put(2 + J, x);
+        }
+      }
+      tc_fence_before();
+      // the chunk's decay multiplies the state once a chunk: exact (while the other
+      // warps invert)
+      double gtot = 0.;
+      const float con0 = con;
+      if (pw == 3) {
+        gtot = exp2((double)g63x * 0x1p-44);
+        if (hj + 1 < tp.share) gates(hd + 1, gb ^ 1);
+      }
+      if (isk) {
+        // the inverses of this warp's two diagonal blocks, a column a lane
+        __syncwarp();
+        const int o = 32 * pw + (lane & 16), col = lane & 15;
+        f2 x[8];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          f2 a0 = mk2(col == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
+#pragma unroll
+          for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
+            const float4 a = *reinterpret_cast<const float4 *>(&s.Am[o + i][o + 4 * j4]);
+            // (columns from i on hold zeros; x not yet set is not read)
+            if (4 * j4 + 1 < i) a0 = fma2(mk2(-a.x, -a.y), x[2 * j4], a0);
+            else a0.x = fmaf(-a.x, x[2 * j4].x, a0.x);
+            if (4 * j4 + 3 < i) a1 = fma2(mk2(-a.z, -a.w), x[2 * j4 + 1], a1);
+            else if (4 * j4 + 2 < i) a1.x = fmaf(-a.z, x[2 * j4 + 1].x, a1.x);
+          }
+          a0 = add2(a0, a1);
+          const float xi = a0.x + a0.y;
+          if (i & 1) x[i / 2].y = xi; else x[i / 2].x = xi;
+        }
+        __syncwarp();  // every lane has read the blocks
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s.Am[o + 2 * i][o + col] = x[i].x;
+          s.Am[o + 2 * i + 1][o + col] = x[i].y;
+        }
+      }
+      __syncthreads();
+      {  // below the diagonal blocks of 16: half pw & 1 of the columns of pair pw / 2
+        const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
+        float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
+        float c1[1][4], c2[1][4];
+        small_product<1, 2, false>(&s.Am[o + 16][o], &s.Am[o][o + n], pw & 1, c1);
+        put_product<1>(scratch, c1, 1.f);
+        __syncwarp();
+        small_product<1, 2, true>(&s.Am[o + 16][o + 16], scratch, 0, c2);
+        __syncthreads();  // A21 has been read
+        put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
+      }
+      __syncthreads();
+      {  // and of 32: eight columns a warp
+        float *scratch = &s.Am[0][32 + 8 * pw];
+        float c1[2][4], c2[2][4];
+        small_product<2, 4, false>(&s.Am[32][0], &s.Am[0][8 * pw], pw, c1);
+        put_product<2>(scratch, c1, 1.f);
+        __syncwarp();
+        small_product<2, 4, true>(&s.Am[32][32], scratch, 0, c2);
+        __syncthreads();
+        put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
+      }
+      __syncthreads();
+      // T diag(b) to float16 pairs: row pt % 64, half pt / 64 (of the first rows
+      // the second half is zero)
+      const int hf = pw >> 1;
+      const bool have = pw != 2;
+      f2 t[16];
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (have) a = *reinterpret_cast<const float4 *>(&s.Am[tok][32 * hf + 4 * q]);
+        const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
+        t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
+        t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
+        sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
+      }
+      sum = warp_max(sum);
+      if (lane == 0) s.tn[pw] = sum;
+      __syncthreads();  // T takes A's place
+      // (a bound of the rows' sums: the largest of each half)
+      const float tn = fmaxf(s.tn[0], s.tn[1]) + fmaxf(s.tn[2], s.tn[3]);
+      int eT = scale_exp(tn);
+      eT = eT < 0 ? eT : 0;
+      const f2 sc = mk2(pow2i(eT), pow2i(eT));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const float4 h = *reinterpret_cast<const float4 *>(&s.h[16 * J + 4 * q]);
-        x[2 * q] = mul2(mul2(mk2(h.x, h.y), mk2(fr, fr)),
-                        mk2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1])));
-        x[2 * q + 1] = mul2(mul2(mk2(h.z, h.w), mk2(fr, fr)),
-                            mk2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3])));
-      }
-    };
-    {
-      f2 x[8];
-      float o[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int j = (tok & ~15) + q;
-        const f2 gj = s.g[j];
-        const f2 d = add2(gi, mk2(-gj.x, -gj.y));
-        const bool in = isk ? j < tok : j <= tok;
-        o[q] = in ? __uint_as_float(own[q]) * (rowf * s.f[j] * ex2(d.x + d.y)) : 0.f;
-      }
-      before(2 * blk, r0, x);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = up ? x[q] : mk2(o[2 * q], o[2 * q + 1]);
-      put(2 * blk, x);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = up ? mk2(o[2 * q], o[2 * q + 1]) : mk2(0.f, 0.f);
-      put(2 * blk + 1, x);
-    }
-#pragma unroll 1
-    for (int J = 0; J < 2; ++J) {
-      f2 x[8];
-      if (blk) {
-        tmem_ld16(grow + 16 * J, r0);
-        tmem_ld_wait();
-        before(J, r0, x);
-        put(J, x);
-      } else if (!isk) {  // above P's diagonal blocks
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = mk2(0.f, 0.f);
-        put(2 + J, x);
-      }
-    }
-    tc_fence_before();
-    // the chunk's decay multiplies the state once a chunk: exact (while the other
-    // warps invert)
-    double gtot = 0.;
-    if (pw == 3) gtot = exp2((double)g63x * 0x1p-44);
-    if (isk) {
-      // the inverses of this warp's two diagonal blocks, a column a lane
-      __syncwarp();
-      const int o = 32 * pw + (lane & 16), col = lane & 15;
-      f2 x[8];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        f2 a0 = mk2(col == i ? 1.f : 0.f, 0.f), a1 = mk2(0.f, 0.f);
-#pragma unroll
-        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-          const float4 a = *reinterpret_cast<const float4 *>(&s.Am[o + i][o + 4 * j4]);
-          // (columns from i on hold zeros; x not yet set is not read)
-          if (4 * j4 + 1 < i) a0 = fma2(mk2(-a.x, -a.y), x[2 * j4], a0);
-          else a0.x = fmaf(-a.x, x[2 * j4].x, a0.x);
-          if (4 * j4 + 3 < i) a1 = fma2(mk2(-a.z, -a.w), x[2 * j4 + 1], a1);
-          else if (4 * j4 + 2 < i) a1.x = fmaf(-a.z, x[2 * j4 + 1].x, a1.x);
+        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+        if (have) {
+          split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
+          split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
+          split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
+          split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
         }
-        a0 = add2(a0, a1);
-        const float xi = a0.x + a0.y;
-        if (i & 1) x[i / 2].y = xi; else x[i / 2].x = xi;
+        *reinterpret_cast<uint4 *>(s.T + sw128(tok, 4 * hf + q)) = hi;
+        *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(tok, 4 * hf + q)) = lo;
       }
-      __syncwarp();  // every lane has read the blocks
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s.Am[o + 2 * i][o + col] = x[i].x;
-        s.Am[o + 2 * i + 1][o + col] = x[i].y;
+      if (pw == 3 && lane == 0) {
+        fac[4 * kC] = (float)gtot;
+        fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
+        fac[4 * kC + 2] = tn * sc.x;
+        fac[4 * kC + 3] = (float)eT;
+        fac[4 * kC + 4] = con0;
+        fac[4 * kC + 5] = ok ? 0.f : 1.f;
       }
-    }
-    __syncthreads();
-    {  // below the diagonal blocks of 16: half pw & 1 of the columns of pair pw / 2
-      const int o = 32 * (pw >> 1), n = 8 * (pw & 1);
-      float *scratch = &s.Am[16 * (pw >> 1)][32 + n];  // (of the block above the diagonal)
-      float c1[1][4], c2[1][4];
-      small_product<1, 2, false>(&s.Am[o + 16][o], &s.Am[o][o + n], pw & 1, c1);
-      put_product<1>(scratch, c1, 1.f);
-      __syncwarp();
-      small_product<1, 2, true>(&s.Am[o + 16][o + 16], scratch, 0, c2);
-      __syncthreads();  // A21 has been read
-      put_product<1>(&s.Am[o + 16][o + n], c2, -1.f);
-    }
-    __syncthreads();
-    {  // and of 32: eight columns a warp
-      float *scratch = &s.Am[0][32 + 8 * pw];
-      float c1[2][4], c2[2][4];
-      small_product<2, 4, false>(&s.Am[32][0], &s.Am[0][8 * pw], pw, c1);
-      put_product<2>(scratch, c1, 1.f);
-      __syncwarp();
-      small_product<2, 4, true>(&s.Am[32][32], scratch, 0, c2);
+      fence_async_smem();
+      tc_fence_before();
       __syncthreads();
-      put_product<2>(&s.Am[32][8 * pw], c2, -1.f);
-    }
-    __syncthreads();
-    // T diag(b) to float16 pairs: row pt % 64, half pt / 64 (of the first rows
-    // the second half is zero)
-    const int hf = pw >> 1;
-    const bool have = pw != 2;
-    f2 t[16];
-    float sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (have) a = *reinterpret_cast<const float4 *>(&s.Am[tok][32 * hf + 4 * q]);
-      const float4 b = *reinterpret_cast<const float4 *>(&s.bv[32 * hf + 4 * q]);
-      t[2 * q] = mul2(mk2(a.x, a.y), mk2(b.x, b.y));
-      t[2 * q + 1] = mul2(mk2(a.z, a.w), mk2(b.z, b.w));
-      sum += (fabsf(t[2 * q].x) + fabsf(t[2 * q].y)) + (fabsf(t[2 * q + 1].x) + fabsf(t[2 * q + 1].y));
-    }
-    sum = warp_max(sum);
-    if (lane == 0) s.tn[pw] = sum;
-    __syncthreads();  // T takes A's place
-    // (a bound of the rows' sums: the largest of each half)
-    const float tn = fmaxf(s.tn[0], s.tn[1]) + fmaxf(s.tn[2], s.tn[3]);
-    int eT = scale_exp(tn);
-    eT = eT < 0 ? eT : 0;
-    const f2 sc = mk2(pow2i(eT), pow2i(eT));
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-      if (have) {
-        split_h2(mul2(t[4 * q], sc), hi.x, lo.x);
-        split_h2(mul2(t[4 * q + 1], sc), hi.y, lo.y);
-        split_h2(mul2(t[4 * q + 2], sc), hi.z, lo.z);
-        split_h2(mul2(t[4 * q + 3], sc), hi.w, lo.w);
+      tc_fence_after();
+      if (pt == 0) {
+        uint8_t *out = tp.rec + (rs * p.H + hd) * (int64_t)sizeof(Rec);
+        bulk_store(out, s.T, kRecT);
+        bulk_store(out + kRecT, s.rest, sizeof(Rec) - kRecT);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
-      *reinterpret_cast<uint4 *>(s.T + sw128(tok, 4 * hf + q)) = hi;
-      *reinterpret_cast<uint4 *>(s.T + kC * 128 + sw128(tok, 4 * hf + q)) = lo;
-    }
-    if (pw == 3 && lane == 0) {
-      fac[4 * kC] = (float)gtot;
-      fac[4 * kC + 1] = fmaxf(s.ekn[0], s.ekn[1]);
-      fac[4 * kC + 2] = tn * sc.x;
-      fac[4 * kC + 3] = (float)eT;
-      fac[4 * kC + 4] = con;
-      fac[4 * kC + 5] = ok ? 0.f : 1.f;
-    }
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (pt == 0) {
-      uint8_t *out = tp.rec + unit * (int64_t)sizeof(Rec);
-      bulk_store(out, s.T, kRecT);
-      bulk_store(out + kRecT, s.rest, sizeof(Rec) - kRecT);
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
   }
   if (pt == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -1595,7 +1614,11 @@ cudaError_t launch_gdr_tc(const GdrParams &p, void *workspace, cudaStream_t s) {
   GdrTcParams q;
   q.p = p;
   q.vtiles = (p.V + kV - 1) / kV;
-  q.units = slots_of(p) * p.H;
+  // (shared keys: once for all their value heads where there are chunks enough to
+  // fill the SMs that way, twice over: 8 x 2048 tokens of 32 heads on 16 key heads
+  // 117 us, head by head 123)
+  q.share = p.H > p.Hk && slots_of(p) * p.Hk >= 12ll * device_sm_count() ? p.H / p.Hk : 1;
+  q.units = slots_of(p) * p.H / q.share;
   q.chunks = p.cu ? 0 : (p.L + kC - 1) / kC;
   q.rec = static_cast<uint8_t *>(workspace) + kGdrStatusBytes;
   q.keys = q.rec + (size_t)(slots_of(p) * p.H) * sizeof(Rec);

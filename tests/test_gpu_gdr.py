@@ -196,6 +196,53 @@ def test_scan_few_long(cuda_ok, n, L, hk, h, K, V):
     _close(hl, rh, "h_last")
 
 
+@pytest.mark.parametrize("packed", [False, True])
+def test_scan_many_chunks_of_shared_keys(cuda_ok, packed):
+    """Chunks enough that the heads that share keys are prepared together."""
+    n, L, hk, h, K, V = 60, 970, 2, 6, 64, 64
+    d = I.gdr_inputs(n, L, hk, h, K, V, io="bf16", seed=7, h0=True)
+    g = _dev(d)
+    if packed:
+        cu = torch.arange(0, n * L + 1, L, dtype=torch.int32, device="cuda")
+        y, hl = _scan({k: x.flatten(0, 1)[None] if k in ("q", "k", "v", "dt", "beta") else x for k, x in g.items()},
+                      cu_seqlens=cu)
+        y = y.reshape(n, L, h, V)
+    else:
+        y, hl = _scan(g)
+    some = [0, 33, 59]
+    part = {k: x[some] if k not in ("A", "dt_bias") else x for k, x in d.items()}
+    ry, rh, _ = _ref(part)
+    _close(y[some], ry, "y")
+    _close(hl[some], rh, "h_last")
+
+
+def test_scan_segments_in_a_graph(cuda_ok):
+    """All launches of a cut sequence, captured and replayed on new inputs, and
+    two such calls at once on streams of their own: the same bits."""
+    ops = _ops()
+    d = _dev(I.gdr_inputs(1, 2500, 1, 2, 128, 128, seed=13, h0=True))
+    y0, h0 = _scan(d)
+    ops.check_every_call(False)
+    try:
+        e = {x: d[x].clone() for x in d}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            yg, hg = _scan(e)
+        for seed in (14, 13):
+            new = _dev(I.gdr_inputs(1, 2500, 1, 2, 128, 128, seed=seed, h0=True))
+            for x in e:
+                e[x].copy_(new[x])
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(yg, y0) and torch.equal(hg, h0)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        outs = [_scan(d, stream=s) for s in streams for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, y0) and torch.equal(h, h0) for y, h in outs)
+    finally:
+        ops.check_every_call(True)
+
+
 def test_scan_few_long_packed(cuda_ok):
     """The same, packed: segments of very different lengths, some of them and
     one sequence empty, states updated in place, one sequence skipped."""
