@@ -521,11 +521,21 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  *            one slot race on it).
  *   An empty sequence copies its state from h0 (or zeros) to h_last.
  *   workspace: gdr_chunk_scan_workspace() bytes, or NULL if that is 0.  Word 0
- *            is the call's status word, as for ssm_scan_fwd.
+ *            is the call's status word, as for ssm_scan_fwd.  The query wants
+ *            the call's sizes, strides and flags, and cu_seqlens set or not as
+ *            in the call; other pointers are not looked at.
  *
- * bf16 with key_dim <= 128 runs on the tensor cores, 64 tokens a chunk; a
- * value that is not finite then also reaches earlier tokens of its chunk.
- * Everything else runs token by token in float32.  key_dim 1..256.
+ * With more than 1024 sequences the bounds must not decrease; sequences that
+ * overlap have unspecified results.
+ *
+ * bf16 runs on the tensor cores, 64 tokens a chunk, where key_dim <= 128 and
+ * key_dim, value_dim and the strides of q, k and v are multiples of 8 (the
+ * workspace then holds 25.7 KB a chunk and head and 16 KB a chunk and key
+ * head); a value that is not finite then also reaches earlier tokens of its
+ * chunk.  Few long sequences with GDR_QK_L2NORM are cut into segments that run
+ * side by side.  Everything else, and sequences of up to 64 tokens where that
+ * is faster, runs token by token in float32.  key_dim 1..256.  The state is
+ * float32 throughout, its products with keys of bf16 calls of 22 bits a factor.
  * ---------------------------------------------------------------------- */
 #define GDR_BETA_SIGMOID 8u
 #define GDR_QK_L2NORM 16u

@@ -192,3 +192,33 @@ def test_oracle_full_strength_recalls():
     v = rng.normal(size=(1, 4, 1, 2))
     y, S, _ = O.gdr_scan(k, k, v, None, None, np.ones((1, 4, 1)), scale=1.0, flags=16, l2_eps=0.0)
     assert np.allclose(y, v)
+
+
+def test_scan_wants_its_workspace(lib):
+    """The tensor-core shapes need one, the others do not; too small is refused."""
+    n = ctypes.c_size_t(1)
+    for kw, need in ((dict(seqlen=640), True), (dict(seqlen=640, io=0), False), (dict(seqlen=640, key_dim=132), False),
+                     (dict(seqlen=640, q_row=260, key_dim=64), False), (dict(seqlen=640, value_dim=100), False),
+                     (dict(seqlen=16), False)):
+        a = _scan(**kw)
+        assert lib.gdr_chunk_scan_workspace(ctypes.byref(a), ctypes.byref(n)) == OK
+        assert (n.value > 0) == need, kw
+    a = _scan(seqlen=640)
+    lib.gdr_chunk_scan_workspace(ctypes.byref(a), ctypes.byref(n))
+    assert lib.gdr_chunk_scan_fwd(ctypes.byref(a), None) == WS
+    a.workspace, a.workspace_bytes = P, n.value - 1
+    assert lib.gdr_chunk_scan_fwd(ctypes.byref(a), None) == WS
+
+
+@pytest.mark.parametrize("pack,cls,name", [
+    (L.GDR_SCAN, L.GdrScanArgs, "gdr_scan_args"), (L.GDR_STEP, L.GdrStepArgs, "gdr_step_args"),
+    (L.GDR_NORM, L.GdrNormArgs, "gdr_norm_args"), (L.CONV_PACKED, L.ConvPackedArgs, "ssm_conv_packed_args")])
+def test_packed_arguments_are_the_structures(pack, cls, name):
+    """Every field lands where the C structure has it."""
+    fields = cls._fields_
+    for at in range(len(fields)):
+        values = [0.0 if t is ctypes.c_float else 0 for _, t in fields]
+        values[at] = 1.5 if fields[at][1] is ctypes.c_float else 77
+        got = cls.from_buffer_copy(pack(*values))
+        for (field, t), v in zip(fields, values):
+            assert (getattr(got, field) or 0) == v, (name, field)
