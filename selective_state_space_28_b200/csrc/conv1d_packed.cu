@@ -110,17 +110,31 @@ template <int N> __device__ __forceinline__ void store_floats(float *p, const fl
   }
 }
 
-// The sequence with run `run`, by a whole warp: among up to 1024 by looking at
-// all (one round of loads; -1: none), among more by bisection.
+// Whether run `run` is one of sequence i's (a valid pair of bounds, a slot that
+// is not padding).
+template <int RUN>
+__device__ __forceinline__ bool has_run(const ConvPackedParams &p, int64_t i, int64_t run) {
+  const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / RUN + i;
+  const int64_t slot = p.slots ? (int64_t)p.slots[i] : 0;
+  return b >= 0 && e > b && e <= p.tokens && first <= run && run < first + (e - b + RUN - 1) / RUN &&
+         (!p.slots || (slot >= 0 && slot < p.state_rows));
+}
+
+// The sequence with run `run`, by a whole warp (-1: none).  The last whose first
+// run is not after it has it where the bounds do not decrease: among up to 1024
+// by counting (one round of loads), among more by bisection.  Where it does not,
+// the up to 1024 are looked through.
 template <int RUN>
 __device__ __forceinline__ int64_t find_sequence(const ConvPackedParams &p, int64_t run) {
   if (p.nseq <= 1024) {
+    const int lane = threadIdx.x & 31;
+    int n = 0;
+    for (int i = lane; i < (int)p.nseq; i += 32) n += (int64_t)p.cu[i] / RUN + i <= run;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n > 0 && has_run<RUN>(p, n - 1, run)) return n - 1;
     int at = -1;
-    for (int i = threadIdx.x & 31; i < (int)p.nseq; i += 32) {
-      const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / RUN + i;
-      if (b < 0 || e <= b || e > p.tokens || first > run || run >= first + (e - b + RUN - 1) / RUN) continue;
-      if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = i;
-    }
+    for (int i = lane; i < (int)p.nseq; i += 32)
+      if (has_run<RUN>(p, i, run)) at = i;
     return __reduce_max_sync(0xffffffffu, at);
   }
   int64_t lo = 0, hi = p.nseq - 1;
