@@ -10,35 +10,37 @@
 //   y_i = scale (e^g_i S^T q_i + sum_{j<=i} e^(g_i - g_j) (q_i.k_j) U_j),
 //   S  <- e^g_63 S + sum_j e^(g_63 - g_j) k_j U_j^T.
 //
-// Two kernels.  The first is parallel over chunks: one CTA per (chunk, value
-// head) makes what needs no state, T = (I + A)^-1, P_ij = e^(g_i - g_j) q_i.k_j
-// (j <= i) and the tokens' factors, and leaves them in the workspace as the
-// second one's shared-memory image (26 KB a chunk and head).  The second walks
-// the chunks, one CTA per (sequence, value head, 128 value columns).  A TMEM
-// lane is a value column, so every product has M = 128 and its A operand (S, R,
-// U, transposed) comes from TMEM, where the thread that owns the lane wrote
-// it; tokens and key dimensions are columns:
+// Two kernels.  The first is parallel over chunks: for each and each value head
+// it makes what needs no state, T = (I + A)^-1 diag(b), P_ij = e^(g_i - g_j)
+// q_i.k_j (j <= i) and the tokens' factors, and leaves them in the workspace as
+// the second one's shared-memory image (26 KB), with the chunk's scaled keys for
+// each key head.  The second walks the chunks, one CTA per (sequence, value
+// head, 128 value columns).  A TMEM lane is a value column, so every product has
+// M = 128 and its A operand (S, R, U, transposed) comes from TMEM, where the
+// thread that owns the lane wrote it; tokens and key dimensions are columns:
 //
-//   KS = S^T K^T, QS = S^T Q^T        B = the keys / queries, K-major
-//   U  = R T^T                        B = T
-//   PU = U P^T                        B = P
+//   KS = S^T K^T                      B = the keys, K-major
+//   U  = R T^T, R = v - e^g KS        B = T
+//   Y  = S^T (e^g Q)^T + U P^T        B = the queries with their decays, and P
 //   dS = U'^T K, U'_j = e^(g_63 - g_j) U_j   B = the keys, MN-major
 //
 // The chain KS -> R -> U -> U' -> dS -> S bounds it: three products one behind
-// the other and the elementwise work between them, each with its latency.  QS,
-// PU, y and the next chunk's conversion run beside it; the state goes in two
-// halves of key dimensions, so that dS of one half and KS of the other run
-// under the elementwise work.
+// the other and the elementwise work between them, each with its latency
+// (commit, wake-up, TMEM loads and stores).  Y and the next chunk's conversion
+// run beside it; the state goes in two halves of key dimensions, so that KS of
+// one half runs under the elementwise work of the other.  8 x 2048 tokens of 32
+// heads, 128 x 128: 117 us + 200 us, 5200 cycles a chunk, 1600 of them the
+// chain's products.
 //
 // Precision.  The state is kept and returned in float32, so what feeds it may
 // not round to 16 bits: the products run on float16 pairs, x = hi + lo (22
 // bits), two (KS, dS) or three (U) products for one.  y is returned in
-// bfloat16: for QS and PU the hi parts alone do (2^-11 of a term beside the
+// bfloat16: for Y the hi parts alone do (2^-11 of a term beside the
 // result's 2^-8).  float16 has the digits but not the range, so every operand
 // is scaled by powers of two: a key or query by its own (its norm comes to
 // 1 .. 2; a bfloat16's 8 bits stay exact down to 2^-17 of that), the norm
 // factors being applied in float32, and S, R, U each by one for 32 value
-// columns and a chunk, from bounds on measured maxima, so that the largest
+// columns and a chunk, from bounds on the measured largest S and v, so that the largest
 // value stays below 2^15 and one 2^-18 of it still has 22 bits.  A warp's
 // lanes that are not finite do not count toward the maxima.
 //
@@ -283,13 +285,14 @@ __device__ __forceinline__ void put_product(float *o, const float (&c)[MT][4], f
           make_float2(sign * c[m][2 * e], sign * c[m][2 * e + 1]);
 }
 
-// CTAs of 128 threads, six to an SM, each over (chunk, value head) units (a
-// launch of one CTA a unit left a third of the slots empty).  Row pt of [K; Q] [K]^T is
-// thread pt's (TMEM lane pt): keys' rows make A, queries' P.  The inverse goes
-// by blocks: the four 16 x 16 diagonal blocks by forward substitution, a column
-// a lane; then twice -T22 A21 T11 for the block below two of them, the products
-// as float32 on mma (a multiply-add version read its operands from shared memory
-// four times as often, which bound the kernel: 4200 cycles a unit of SM time).
+// CTAs of 128 threads, six to an SM, each over (chunk, value head) units.  Row pt
+// of [K; Q] [K]^T is thread pt's (TMEM lane pt): keys' rows make A, queries' P.
+// The inverse goes by blocks: the four 16 x 16 diagonal blocks by forward
+// substitution, a column a lane; then twice -T22 A21 T11 for the block below two
+// of them, the products as float32 on mma (a multiply-add version read its
+// operands from shared memory four times as often, which bound the kernel: 4200
+// cycles a unit of SM time).  Bound by issue: 8500 warp instructions a unit, half
+// of the slots taken; barriers and instruction fetch are the largest stalls.
 template <int KD>
 __global__ void __launch_bounds__(kPrepThreads, 6)
     gdr_prep_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mQ,
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
 //          the product with T; the state from dS.
 //   8-11   queries to scaled float16, in place, and the chunk's bounds, a chunk
 //          ahead.
-//   12-15  y from QS and PU, a chunk behind.
+//   12-15  y from Y, a chunk behind.
 //   16     copies of the scaled keys and of Q ([64 x 64] slabs, 128-byte swizzle,
 //          three stages).
 //   17     MMA issuer.
@@ -846,7 +849,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq = pick;
   }
   int64_t slot, t0, len;
-  if (!gdr_sequence(p, seq, slot, t0, len)) return;
+  if (!gdr_sequence(p, seq, slot, t0, len)) {
+    pdl_wait();  // (no CTA ends before the kernels ahead have)
+    return;
+  }
   const int64_t g = hd / (p.H / p.Hk);
   int64_t slot0 = first_slot(tp, seq, t0);
   if (PASS) {
@@ -883,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (nch == 0) {  // an empty sequence or segment hands its state on
-    if (PASS) pdl_wait();  // (and no later kernel runs ahead of an earlier one)
+    pdl_wait();
     if (warp < 8 && dst && live) {
       for (int r = ch; r < p.K; r += 2) dst[(int64_t)r * cols + cv] = start(r);
     }
