@@ -535,7 +535,9 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  * chunk.  Few long sequences with GDR_QK_L2NORM are cut into segments that run
  * side by side.  Everything else, and sequences of up to 64 tokens where that
  * is faster, runs token by token in float32.  key_dim 1..256.  The state is
- * float32 throughout, its products with keys of bf16 calls of 22 bits a factor.
+ * float32 throughout, its products with keys of bf16 calls of 22 bits a factor:
+ * their errors are relative to the largest values within a chunk, so a state
+ * that decays by 2^20 within 64 tokens onto far smaller values keeps fewer digits.
  * ---------------------------------------------------------------------- */
 #define GDR_BETA_SIGMOID 8u
 #define GDR_QK_L2NORM 16u
