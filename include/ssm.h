@@ -525,8 +525,9 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  *            the call's sizes, strides and flags, and cu_seqlens set or not as
  *            in the call; other pointers are not looked at.
  *
- * With more than 1024 sequences the bounds must not decrease; sequences that
- * overlap have unspecified results.
+ * Up to 1024 sequences may lie in any order among the rows (a pair that goes
+ * back between them is an empty sequence); with more the bounds must not
+ * decrease.  Sequences that overlap have unspecified results.
  *
  * bf16 runs on the tensor cores, 64 tokens a chunk, where key_dim <= 128 and
  * key_dim, value_dim and the strides of q, k and v are multiples of 8 (the

@@ -102,11 +102,13 @@ struct GdrTcParams {
   float *seg_state, *seg_map;
 };
 
-// The record of chunk 0 of sequence `seq`.  Packed sequences start at
-// cu / 64 + seq: behind all chunks of the ones before, as theirs number at
-// most (length / 64, rounded down) + 1.
-__device__ __forceinline__ int64_t first_slot(const GdrTcParams &tp, int64_t seq, int64_t t0) {
-  return tp.chunks ? seq * tp.chunks : t0 / kC + seq;
+// The record of the chunk that starts at row t0 of sequence `seq`, its chunk c.
+// Packed, a sequence's first chunk has one of its own, number rows / 64 + seq, and
+// a later chunk the number t0 / 64 - 1, whatever the order of the sequences: the 64
+// rows before such a chunk are its own sequence's, so that among sequences that are
+// apart no two such chunks start within the same 64 rows.
+__device__ __forceinline__ int64_t record_slot(const GdrTcParams &tp, int64_t seq, int64_t t0, int64_t c) {
+  return tp.chunks ? seq * tp.chunks + c : c == 0 ? tp.p.rows / kC + seq : t0 / kC - 1;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -326,18 +328,20 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
   for (int64_t unit = blockIdx.x; unit < tp.units; unit += gridDim.x) {
     // the sequence and chunk of this record
     const int64_t groups = p.H / tp.share, rs = unit / groups, hd0 = unit % groups * tp.share;
-    round ^= 1;
     int64_t seq, c, slot, t0, len;
     if (tp.chunks) {
       seq = rs / tp.chunks;
     } else {
-      if (p.nseq <= kSearched) {
+      if (rs >= p.rows / kC) {  // a first chunk
+        seq = rs - p.rows / kC;
+      } else if (p.nseq <= kSearched) {
         // (among all: bounds that are out of order and sequences that are skipped
         // leave the others right)
+        round ^= 1;
         int at = -1;
         for (int64_t i = pt; i < p.nseq; i += kPrepThreads) {
-          const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / kC + i;
-          if (b < 0 || e <= b || e > p.rows || first > rs || rs >= first + (e - b + kC - 1) / kC) continue;
+          const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / kC;
+          if (b < 0 || e <= b || e > p.rows || first > rs || rs >= first + (e - b - 1) / kC) continue;
           if (!p.slots || (p.slots[i] >= 0 && p.slots[i] < p.state_rows)) at = (int)i;
         }
         at = __reduce_max_sync(0xffffffffu, at);
@@ -349,15 +353,15 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
         int64_t lo = 0, hi = p.nseq - 1;
         while (lo < hi) {
           const int64_t mid = (lo + hi + 1) >> 1;
-          if ((int64_t)p.cu[mid] / kC + mid <= rs) lo = mid;
+          if (p.cu[mid] / kC <= rs) lo = mid;
           else hi = mid - 1;
         }
-        seq = lo;
+        seq = p.cu[lo] / kC <= rs ? lo : -1;
       }
       if (seq < 0) continue;
     }
     if (!gdr_sequence(p, seq, slot, t0, len)) continue;
-    c = rs - first_slot(tp, seq, t0);
+    c = tp.chunks ? rs - seq * tp.chunks : rs >= p.rows / kC ? 0 : rs - t0 / kC + 1;
     if (c < 0 || c * kC >= len) continue;
     const int64_t left = len - c * kC;
     const int nv = (int)(left < kC ? left : kC);
@@ -854,14 +858,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   const int64_t g = hd / (p.H / p.Hk);
-  int64_t slot0 = first_slot(tp, seq, t0);
+  int64_t c0 = 0;  // the segment's first chunk
   if (PASS) {
-    const int64_t all = (len + kC - 1) / kC, c0 = all * seg / tp.nseg, c1 = all * (seg + 1) / tp.nseg;
-    slot0 += c0;
+    const int64_t all = (len + kC - 1) / kC, c1 = all * (seg + 1) / tp.nseg;
+    c0 = all * seg / tp.nseg;
     t0 += c0 * kC;
     len = (c1 * kC < len ? c1 * kC : len) - c0 * kC;
   }
   const int nch = (int)((len + kC - 1) / kC);
+  // the records of the first chunk here and, one behind the other, of the rest
+  const int64_t slot0 = record_slot(tp, seq, t0, c0), slot1 = record_slot(tp, seq, t0 + kC, c0 + 1);
   const int64_t v0 = vt * kV;
   const int64_t cols = map ? p.K : p.V;
   // where the state comes from and goes to: its first value column here
@@ -933,7 +939,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 16 && lane == 0) {
       // ---------------------------------------------------------- keys and queries
       tma_prefetch_desc(&mQ);
-      const uint8_t *keys = tp.keys + (slot0 * p.Hk + g) * (int64_t)(NP * kSlab);
+      const int64_t step = p.Hk * (int64_t)(NP * kSlab);
+      const uint8_t *keys = tp.keys + slot0 * step + g * (int64_t)(NP * kSlab);
       pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
@@ -942,23 +949,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_expect_tx(&s.fullk[k3], NP * 128 * 128);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
-          bulk_load(s.kq[k3][n], keys + (c * p.Hk * NP + n) * (int64_t)kSlab, kSlab, &s.fullk[k3]);
+          bulk_load(s.kq[k3][n], keys + n * kSlab, kSlab, &s.fullk[k3]);
           tma_load_3d(s.kq[k3][n] + kC * 128, &mQ, &s.fullk[k3], 64 * n, (int)g, t);
         }
+        keys += c ? step : (slot1 - slot0) * step;
       }
       if (c < nch && tp.status) atomicExch(tp.status, 2);
       // Leave no copy in flight: the last chunks issued have landed.
       for (int i = c > 3 ? c - 3 : 0; i < c; ++i) mbar_wait(&s.fullk[i % 3], (i / 3) & 1, kWaitLimit);
     } else if (warp == 18 && lane == 0) {
       // ---------------------------------------------------------- records
-      const uint8_t *rec = tp.rec + (slot0 * p.H + hd) * (int64_t)sizeof(Rec);
+      const int64_t step = p.H * (int64_t)sizeof(Rec);
+      const uint8_t *rec = tp.rec + slot0 * step + hd * (int64_t)sizeof(Rec);
       pdl_wait();  // the first kernel's work
       int c = 0;
       for (; c < nch; ++c) {
         const int r3 = c % 3;
         if (c >= 3 && !mbar_wait(&s.rfree[r3], (c / 3 - 1) & 1, kWaitLimit)) break;
         mbar_expect_tx(&s.fullr[r3], (uint32_t)sizeof(Rec));
-        bulk_load(&s.rec[r3].r, rec + c * p.H * (int64_t)sizeof(Rec), sizeof(Rec), &s.fullr[r3]);
+        bulk_load(&s.rec[r3].r, rec, sizeof(Rec), &s.fullr[r3]);
+        rec += c ? step : (slot1 - slot0) * step;
       }
       if (c < nch && tp.status) atomicExch(tp.status, 2);
       for (int i = c > 3 ? c - 3 : 0; i < c; ++i) mbar_wait(&s.fullr[i % 3], (i / 3) & 1, kWaitLimit);
@@ -1537,7 +1547,7 @@ bool encode(CUtensorMap *m, const void *ptr, int64_t dim, int64_t heads, int64_t
   return encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, strides, b, sw);
 }
 
-// Records of a call: of every chunk (packed: see first_slot).
+// Records of a call: of every chunk (packed: see record_slot).
 int64_t slots_of(const GdrParams &p) {
   return p.cu ? p.rows / kC + p.nseq : p.nseq * ((p.L + kC - 1) / kC);
 }

@@ -711,3 +711,61 @@ def test_scan_packed_many(cuda_ok):
                                    None, scale=8 ** -1.0)
             _close(y[:, s], ry, "y %d" % i)
             _close(h[i][None], rh, "state %d" % i)
+
+
+def _apart(bounds, rows):
+    """The live sequences of `bounds`, or None where two of them overlap."""
+    live = [(i, b, e) for i, (b, e) in enumerate(zip(bounds, bounds[1:])) if 0 <= b < e <= rows]
+    spans = sorted((b, e) for _, b, e in live)
+    return None if any(x[1] > y[0] for x, y in zip(spans, spans[1:])) else live
+
+
+def _sets_going_back(rows, count, seed):
+    g = np.random.default_rng(seed)
+    sets = [[128, 192, 0, 128], [128, 256, 0, 128], [640, 700, 64, 320, 10, 30], [320, 400, 192, 300, 0, 150]]
+    while len(sets) < count:
+        bounds = [int(x) for x in g.integers(0, rows + 1, g.integers(3, 9))]
+        if any(b > e for b, e in zip(bounds, bounds[1:])) and _apart(bounds, rows):
+            sets.append(bounds)
+    return sets
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_bounds_going_back(cuda_ok, io):
+    """Sequences apart from one another whose bounds lie in any order: each is
+    what it is by itself; the pairs out of order hand their states on, and rows
+    of no sequence stay."""
+    rows, H, K = 1024, 1, 8
+    d = I.gdr_inputs(1, rows, 1, H, K, K, io=io, seed=2)
+    g = _dev(d)
+    sets = _sets_going_back(rows, 240, seed=6)
+    h0 = 0.3 * torch.randn(len(sets), 8, H, K, K, generator=torch.Generator().manual_seed(3))
+    got, want = [], []
+    for bounds, h in zip(sets, h0):
+        n = len(bounds) - 1
+        y = torch.full((1, rows, H, K), 7.0, dtype=g["v"].dtype, device="cuda")
+        g["h0"] = h[:n].cuda()
+        cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        got.append((y, _scan(g, cu_seqlens=cu, y=y)[1]))
+        want += [(b, e, h[i]) for i, b, e in _apart(bounds, rows)]
+    at = 0
+    ref = []
+    for part in (want[i:i + 100] for i in range(0, len(want), 100)):
+        longest = max(e - b for b, e, _ in part)
+        row = torch.stack([torch.arange(longest).clamp(max=e - b - 1) + b for b, e, _ in part])
+        x = {k: d[k][0][row] for k in ("q", "k", "v", "dt", "beta")}
+        ry, _, states = O.gdr_scan(x["q"], x["k"], x["v"], x["dt"], d["A"], x["beta"], d["dt_bias"],
+                                   torch.stack([h for _, _, h in part]), scale=K ** -0.5)
+        ref += [(ry[i, :e - b], states[i, e - b - 1]) for i, (b, e, _) in enumerate(part)]
+    for bounds, h, (y, out) in zip(sets, h0, got):
+        live = _apart(bounds, rows)
+        rest = torch.ones(rows, dtype=torch.bool)
+        for i, b, e in live:
+            _close(y[0, b:e], ref[at][0], "y %s %d" % (bounds, i))
+            _close(out[i], ref[at][1], "state %s %d" % (bounds, i))
+            rest[b:e] = False
+            at += 1
+        none = [i for i in range(len(bounds) - 1) if i not in [j for j, _, _ in live]]
+        assert torch.equal(out[none].cpu(), h[none]), bounds
+        assert (y[0, rest.cuda()] == 7).all(), bounds
+    assert at == len(ref)
