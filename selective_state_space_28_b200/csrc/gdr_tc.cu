@@ -1195,19 +1195,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         mx = map ? 0.f : warp_max(mx);
-        // From m, the largest value of the state entering the chunk, bounds of the
-        // state and U' leaving it, z + w m = n, and from such an n of the chunk
-        // before, bounds of this chunk's R and U, x + y n.  With keys of length at
-        // most 1, write strengths b in 0 .. 2 and no growth, I - b k k^T lengthens
-        // nothing: |S| <= e^g sqrt(K) m + 64 b |v| column by column, |R| <= |v| + |S|
-        // and |U| <= b (|v| + |S|).  Else step by step: |R| <= |v| + |ek k| sqrt(K) m,
-        // |U| <= (T's row sums) |R|, |dS| <= sum |k| |U'| <= 128 |U|.
+        // From m, the largest value of the state entering the chunk, a bound of the
+        // state leaving it, z + w m = n, which is one of its columns' lengths |S|, and
+        // from such an n of the chunk before, bounds of this chunk's R and U, x + y n.
+        // With keys of length at most 1, write strengths b in 0 .. 2 and no growth,
+        // I - b k k^T lengthens nothing: |S| <= e^g sqrt(K) m + 64 b |v| column by
+        // column, |R| <= |v| + |S| and |U| <= b (|v| + |S|).  Else step by step:
+        // |R| <= |v| + |ek k| |S|, |U| <= (T's row sums) |R|, |dS| <= sum |k| |U'|
+        // <= 128 |U|, |S| <= sqrt(K) m before.
         const float b = rc.con;
         if (lane == 0 && rc.expired != 0.f) atomicExch(tp.status, 1);
         float4 f = make_float4(65.f * b * b * mx, b, 65.f * b * b * mx, b * kNorm * rc.gC);
         if (!(b > 0.f)) {
-          const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn * kNorm;
-          f = make_float4(t1 * mx, t1 * en, 128.f * tn * mx, fmaf(128.f * tn, en, fabsf(rc.gC)));
+          const float tn = rc.tn * pow2i(-(int)rc.eT), t1 = fmaxf(1.f, tn), en = rc.ekn;
+          f = make_float4(t1 * mx, t1 * en, 128.f * tn * mx, kNorm * fmaf(128.f * tn, en, fabsf(rc.gC)));
         }
         if (lane == 0) s.bound[c % 3][quarter] = f;
       }

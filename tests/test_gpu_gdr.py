@@ -769,3 +769,22 @@ def test_scan_bounds_going_back(cuda_ok, io):
         assert torch.equal(out[none].cpu(), h[none]), bounds
         assert (y[0, rest.cuda()] == 7).all(), bounds
     assert at == len(ref)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_scan_mixed_strengths(cuda_ok, io):
+    """Write strengths below zero in one chunk and none in the next, whose key
+    lies along a state that is the same in all its rows: what is read of it is
+    sqrt(K) times its values."""
+    d = I.gdr_inputs(1, 200, 1, 1, 128, 64, io=io, seed=15, h0=True)
+    d["h0"][:] = 1
+    d["dt"] = None
+    d["beta"][:] = 0.5
+    d["beta"][:, :64] = 2.0 ** -30
+    d["beta"][:, 5] = -2.0 ** -30
+    d["k"][:, 64] = 1
+    d["v"] = d["v"] * 2.0 ** -20
+    y, h = _scan(_dev(d), flags=16)
+    ry, rh, _ = _ref(d, flags=16)
+    _close(y, ry, "y")
+    _close(h, rh, "h_last")
