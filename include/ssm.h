@@ -494,7 +494,8 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  *
  * with S starting from the sequence's state (zeros if h0 == NULL); y_t reads
  * the state after token t's write.  dt == NULL: no decay (a = 1; A and
- * dt_bias are not read).
+ * dt_bias are not read).  Nothing may make the state grow: steps d are not
+ * negative, and b |k|^2 lies in 0 .. 2.
  *
  *   q, k   : [batch, seqlen, key_heads, key_dim]    io type
  *   v      : [batch, seqlen, heads, value_dim]      io type
@@ -533,12 +534,16 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  * key_dim, value_dim and the strides of q, k and v are multiples of 8 (the
  * workspace then holds 25.7 KB a chunk and head and 16 KB a chunk and key
  * head); a value that is not finite then also reaches earlier tokens of its
- * chunk.  Few long sequences with GDR_QK_L2NORM are cut into segments that run
- * side by side.  Everything else, and sequences of up to 64 tokens where that
+ * chunk.  Few long sequences with GDR_QK_L2NORM and GDR_BETA_SIGMOID are cut into
+ * segments that run side by side.  Everything else, and sequences of up to 64 tokens where that
  * is faster, runs token by token in float32.  key_dim 1..256.  The state is
  * float32 throughout, its products with keys of bf16 calls of 22 bits a factor:
  * their errors are relative to the largest values within a chunk, so a state
  * that decays by 2^20 within 64 tokens onto far smaller values keeps fewer digits.
+ * (Where the state may grow all the same, the call by token follows the formula;
+ * on the tensor cores a step of -0.2 / A and less is too much for y within 64
+ * tokens, and a strength of 4 under a key of length 1 costs 2e-6 of the state's
+ * largest value, one of 30 8e-5, and several under the same key all digits.)
  * ---------------------------------------------------------------------- */
 #define GDR_BETA_SIGMOID 8u
 #define GDR_QK_L2NORM 16u

@@ -1520,11 +1520,13 @@ __global__ void __launch_bounds__(256) gdr_carry_kernel(const GdrTcParams tp) {
 // state (the same kernel, from the identity and without values); the carry
 // joins them; a second pass runs segments 1 .. n - 1 from their states.  That
 // is 2 / n of the chunks, about 1.3 us a carry and 20 us of launches, as long
-// as each pass finds an SM for every CTA.  Only for keys of length at most 1,
-// whose maps do not grow.
+// as each pass finds an SM for every CTA.  Only where no map can grow, and so lose
+// the digits of what it leaves as it is: keys of length at most 1, written with
+// strengths of a sigmoid (and no decay above 1).
 int segments_of(const GdrParams &p) {
   const int64_t vt = (p.V + kV - 1) / kV, base = p.nseq * p.H * vt, sms = device_sm_count();
-  if (!(p.flags & GDR_QK_L2NORM) || base * 3 > sms) return 1;
+  const uint32_t bounded = GDR_QK_L2NORM | GDR_BETA_SIGMOID;
+  if ((p.flags & bounded) != bounded || base * 3 > sms) return 1;
   const int64_t chunks = p.rows / kC / p.nseq;
   int best = 1;
   double least = 0.9 * 2.75 * (double)chunks;

@@ -788,3 +788,27 @@ def test_scan_mixed_strengths(cuda_ok, io):
     ry, rh, _ = _ref(d, flags=16)
     _close(y, ry, "y")
     _close(h, rh, "h_last")
+
+
+@pytest.mark.parametrize("flags", [17, 25])
+@pytest.mark.parametrize("L", [3000, 8192])
+def test_scan_few_long_strengths(cuda_ok, L, flags):
+    """Long sequences whose write strengths are numbers as they come: tokens of
+    strength 4 under a key of their own, which the state does not hold and
+    whose values are zero, so that nothing grows but what is not there."""
+    K, V = 64, 64
+    d = I.gdr_inputs(1, L, 1, 1, K, V, io="bf16", seed=L, h0=True)
+    d["A"] = d["A"] * 1e-4
+    if not flags & 8:
+        d["beta"] = d["beta"].float().sigmoid().to(d["beta"].dtype)
+        d["k"][..., 0] = 0
+        d["h0"][:, :, 0] = 0
+        at = slice(7, None, 64)
+        d["k"][:, at] = 0
+        d["k"][:, at, :, 0] = 1
+        d["v"][:, at] = 0
+        d["beta"][:, at] = 4
+    y, h = _scan(_dev(d), flags=flags)
+    ry, rh, _ = _ref(d, flags=flags)
+    _close(y, ry, "y")
+    _close(h, rh, "h_last")
