@@ -127,9 +127,9 @@ ssm_status_t check_gdr(const gdr_scan_args_t *a, bool shapes_only) {
   if (a->cu_seqlens ? a->batch != 1 : a->sequences != a->batch) return SSM_ERR_SHAPE;
   if (!a->slots && (a->h0 || a->h_last) && a->state_rows < a->sequences) return SSM_ERR_SHAPE;
   const int64_t rows = a->batch * a->seqlen;
-  if (a->sequences > 0 && rows > 0 &&
-      (!a->q || !a->k || !a->v || !a->beta || (a->dt && !a->A) || !a->y))
-    return SSM_ERR_NULL;
+  if (a->sequences > 0 && rows > 0 && (!a->q || !a->k || !a->v || !a->beta || !a->y)) return SSM_ERR_NULL;
+  // (read for every head, tokens or not)
+  if (a->sequences > 0 && a->dt && !a->A) return SSM_ERR_NULL;
   if (!all_aligned(16, a->q, a->k, a->v, a->A, a->dt_bias, a->h0, a->y, a->h_last, a->workspace) ||
       !all_aligned(a->io == SSM_BF16 ? 2 : 4, a->dt, a->beta) ||
       !all_aligned(4, a->cu_seqlens, a->slots))

@@ -222,3 +222,9 @@ def test_packed_arguments_are_the_structures(pack, cls, name):
         got = cls.from_buffer_copy(pack(*values))
         for (field, t), v in zip(fields, values):
             assert (getattr(got, field) or 0) == v, (name, field)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(q=None, k=None, v=None, beta=None, y=None), dict(cu_seqlens=P)])
+def test_scan_steps_need_their_rates(lib, kw):
+    """Also where there is no token, and only the states are handed on."""
+    assert lib.gdr_chunk_scan_fwd(ctypes.byref(_scan(seqlen=0, A=None, **kw)), None) == NULL
