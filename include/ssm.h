@@ -534,16 +534,20 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  * key_dim, value_dim and the strides of q, k and v are multiples of 8 (the
  * workspace then holds 25.7 KB a chunk and head and 16 KB a chunk and key
  * head); a value that is not finite then also reaches earlier tokens of its
- * chunk.  Few long sequences with GDR_QK_L2NORM and GDR_BETA_SIGMOID are cut into
- * segments that run side by side.  Everything else, and sequences of up to 64 tokens where that
- * is faster, runs token by token in float32.  key_dim 1..256.  The state is
- * float32 throughout, its products with keys of bf16 calls of 22 bits a factor:
- * their errors are relative to the largest values within a chunk, so a state
- * that decays by 2^20 within 64 tokens onto far smaller values keeps fewer digits.
- * (Where the state may grow all the same, the call by token follows the formula;
- * on the tensor cores a step of -0.2 / A and less is too much for y within 64
- * tokens, and a strength of 4 under a key of length 1 costs 2e-6 of the state's
- * largest value, one of 30 8e-5, and several under the same key all digits.)
+ * chunk.  Few long sequences with GDR_QK_L2NORM and GDR_BETA_SIGMOID are cut
+ * into segments that run side by side.  Everything else, and sequences of up to
+ * 64 tokens where that is faster, runs token by token in float32.  key_dim
+ * 1..256.
+ *
+ * The state is float32 throughout.  On the tensor cores its products with keys
+ * are of 22 bits a factor, their errors relative to the largest values within a
+ * chunk, so a state that decays by 2^20 within 64 tokens onto far smaller values
+ * keeps fewer digits; and y's two products take 11 bits a factor (errors of 2^-11
+ * of their terms beside y's own rounding, 2^-9).  A state that grows all the same
+ * follows the formula where it runs by token.  On the tensor cores y overflows
+ * where steps below zero let it grow by e^0.2 a token; and a strength of 4 under a
+ * key of length 1 costs 2e-6 of the state's largest value, one of 30 8e-5, several
+ * under the same key within a chunk every digit.
  * ---------------------------------------------------------------------- */
 #define GDR_BETA_SIGMOID 8u
 #define GDR_QK_L2NORM 16u
