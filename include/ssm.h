@@ -543,7 +543,7 @@ ssm_status_t ssd_attention_fwd(const ssd_attention_args_t *args, void *stream);
  * are of 22 bits a factor, their errors relative to the largest values within a
  * chunk, so a state that decays by 2^20 within 64 tokens onto far smaller values
  * keeps fewer digits; and y's two products take 11 bits a factor (errors of 2^-11
- * of their terms beside y's own rounding, 2^-9).  A state that grows all the same
+ * of their terms beside y's own rounding, 2^-8).  A state that grows all the same
  * follows the formula where it runs by token.  On the tensor cores y overflows
  * where steps below zero let it grow by e^0.2 a token; and a strength of 4 under a
  * key of length 1 costs 2e-6 of the state's largest value, one of 30 8e-5, several

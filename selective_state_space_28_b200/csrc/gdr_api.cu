@@ -60,19 +60,37 @@ ssm_status_t check_heads(const Args *a) {
   return SSM_OK;
 }
 
-// y must not overlap an input of `rows` rows.
+// Bytes of `rows` rows of `width` values, `row` (0 = dense) apart.
+size_t rows_bytes(int32_t io, int64_t rows, int64_t row, int64_t width) {
+  const size_t es = io == SSM_BF16 ? 2 : 4;
+  return rows > 0 ? (size_t)((rows - 1) * (row ? row : width) + width) * es : (size_t)0;
+}
+
+// Whether `out` overlaps an input of a scan or step of `rows` rows and
+// `sequences` sequences, its states aside.
 template <typename Args>
-bool y_overlaps(const Args *a, int64_t rows) {
-  const size_t es = a->io == SSM_BF16 ? 2 : 4;
-  auto bytes = [&](int64_t row, int64_t width) {
-    return rows > 0 ? (size_t)((rows - 1) * (row ? row : width) + width) * es : (size_t)0;
-  };
+bool overlaps_inputs(const Args *a, int64_t rows, int64_t sequences, const void *out, size_t bytes) {
   const int64_t kr = a->key_heads * a->key_dim, vr = a->heads * a->value_dim;
-  const size_t yb = bytes(0, vr);
-  return overlap(a->y, yb, a->q, bytes(a->q_row, kr)) || overlap(a->y, yb, a->k, bytes(a->k_row, kr)) ||
-         overlap(a->y, yb, a->v, bytes(a->v_row, vr)) ||
-         overlap(a->y, yb, a->dt, bytes(a->dt_row, a->heads)) ||
-         overlap(a->y, yb, a->beta, bytes(a->beta_row, a->heads));
+  const size_t hb = a->dt ? (size_t)a->heads * sizeof(float) : 0;  // (not read without steps)
+  return overlap(out, bytes, a->q, rows_bytes(a->io, rows, a->q_row, kr)) ||
+         overlap(out, bytes, a->k, rows_bytes(a->io, rows, a->k_row, kr)) ||
+         overlap(out, bytes, a->v, rows_bytes(a->io, rows, a->v_row, vr)) ||
+         overlap(out, bytes, a->dt, rows_bytes(a->io, rows, a->dt_row, a->heads)) ||
+         overlap(out, bytes, a->beta, rows_bytes(a->io, rows, a->beta_row, a->heads)) ||
+         overlap(out, bytes, a->A, hb) || overlap(out, bytes, a->dt_bias, hb) ||
+         overlap(out, bytes, a->slots, (size_t)sequences * sizeof(int32_t));
+}
+
+template <typename Args>
+size_t state_bytes(const Args *a) {
+  return (size_t)(a->state_rows * a->heads) * (size_t)(a->key_dim * a->value_dim) * sizeof(float);
+}
+
+// Whether `out`, an output of a prompt scan, overlaps an input, h0 among them.
+bool overlaps_scan(const gdr_scan_args_t *a, const void *out, size_t bytes) {
+  return overlaps_inputs(a, a->batch * a->seqlen, a->sequences, out, bytes) ||
+         overlap(out, bytes, a->cu_seqlens, (size_t)(a->sequences + 1) * sizeof(int32_t)) ||
+         (out != a->h0 && overlap(out, bytes, a->h0, state_bytes(a)));
 }
 
 template <typename Args>
@@ -134,9 +152,11 @@ ssm_status_t check_gdr(const gdr_scan_args_t *a, bool shapes_only) {
       !all_aligned(a->io == SSM_BF16 ? 2 : 4, a->dt, a->beta) ||
       !all_aligned(4, a->cu_seqlens, a->slots))
     return SSM_ERR_ALIGN;
-  if (y_overlaps(a, rows)) return SSM_ERR_SHAPE;
-  const size_t sb = (size_t)(a->state_rows * a->heads) * (size_t)(a->key_dim * a->value_dim) * 4;
-  if (a->h0 != a->h_last && overlap(a->h0, sb, a->h_last, sb)) return SSM_ERR_SHAPE;
+  // (h_last may be h0; y may not)
+  const size_t yb = rows_bytes(a->io, rows, 0, a->heads * a->value_dim), sb = state_bytes(a);
+  if (overlaps_scan(a, a->y, yb) || overlap(a->y, yb, a->h0, sb) || overlap(a->y, yb, a->h_last, sb) ||
+      overlaps_scan(a, a->h_last, sb))
+    return SSM_ERR_SHAPE;
   return SSM_OK;
 }
 
@@ -160,7 +180,12 @@ ssm_status_t gdr_chunk_scan_fwd(const gdr_scan_args_t *a, void *stream) {
   const ssm::GdrParams p = scan_params(a);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (!ssm::gdr_tc_supported(p)) return from_cuda(ssm::launch_gdr_recurrent(p, cs));
-  if (!a->workspace || a->workspace_bytes < ssm::gdr_tc_workspace(p)) return SSM_ERR_WORKSPACE;
+  const size_t wb = ssm::gdr_tc_workspace(p);
+  if (!a->workspace || a->workspace_bytes < wb) return SSM_ERR_WORKSPACE;
+  if (overlaps_scan(a, a->workspace, wb) || overlap(a->workspace, wb, a->h0, state_bytes(a)) ||
+      overlap(a->workspace, wb, a->h_last, state_bytes(a)) ||
+      overlap(a->workspace, wb, a->y, rows_bytes(a->io, p.rows, 0, a->heads * a->value_dim)))
+    return SSM_ERR_SHAPE;
   return from_cuda(ssm::launch_gdr_tc(p, a->workspace, cs));
 }
 
@@ -175,8 +200,11 @@ ssm_status_t gdr_scan_step(const gdr_step_args_t *a, void *stream) {
   if (!all_aligned(16, a->q, a->k, a->v, a->A, a->dt_bias, a->state_io, a->y) ||
       !all_aligned(a->io == SSM_BF16 ? 2 : 4, a->dt, a->beta) || !all_aligned(4, a->slots))
     return SSM_ERR_ALIGN;
-  if (y_overlaps(a, a->batch)) return SSM_ERR_SHAPE;
+  const size_t yb = rows_bytes(a->io, a->batch, 0, a->heads * a->value_dim), sb = state_bytes(a);
   if (a->batch == 0) return SSM_OK;
+  if (overlaps_inputs(a, a->batch, a->batch, a->y, yb) || overlaps_inputs(a, a->batch, a->batch, a->state_io, sb) ||
+      overlap(a->y, yb, a->state_io, sb))
+    return SSM_ERR_SHAPE;
   ssm::GdrParams p;
   fill_heads(p, a);
   p.nseq = a->batch;
@@ -243,10 +271,16 @@ ssm_status_t ssm_conv1d_packed_fwd(const ssm_conv_packed_args_t *a, void *stream
   const size_t xb = work ? (size_t)((a->tokens - 1) * xr + a->channels) * es : 0;
   const size_t ub = work ? (size_t)(a->tokens * a->channels) * es : 0;
   const size_t sb = (size_t)(a->state_rows * a->channels) * (size_t)(a->width - 1) * 4;
-  if (overlap(a->x, xb, a->u, ub) || overlap(a->state_io, sb, a->u, ub) ||
-      overlap(a->state_io, sb, a->x, xb))
-    return SSM_ERR_SHAPE;
   if (!work) return SSM_OK;
+  auto overlaps_inputs = [&](const void *out, size_t bytes) {
+    return overlap(out, bytes, a->x, xb) ||
+           overlap(out, bytes, a->w, (size_t)(a->channels * a->width) * sizeof(float)) ||
+           overlap(out, bytes, a->bias, (size_t)a->channels * sizeof(float)) ||
+           overlap(out, bytes, a->cu_seqlens, (size_t)(a->sequences + 1) * sizeof(int32_t)) ||
+           overlap(out, bytes, a->slots, (size_t)a->sequences * sizeof(int32_t));
+  };
+  if (overlaps_inputs(a->u, ub) || overlaps_inputs(a->state_io, sb) || overlap(a->state_io, sb, a->u, ub))
+    return SSM_ERR_SHAPE;
   ssm::ConvPackedParams p;
   p.tokens = a->tokens;
   p.Cc = a->channels;

@@ -228,3 +228,43 @@ def test_packed_arguments_are_the_structures(pack, cls, name):
 def test_scan_steps_need_their_rates(lib, kw):
     """Also where there is no token, and only the states are handed on."""
     assert lib.gdr_chunk_scan_fwd(ctypes.byref(_scan(seqlen=0, A=None, **kw)), None) == NULL
+
+
+HERE = FAR + (1 << 32)  # a place of its own
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=HERE, h0=HERE + 1024), dict(y=HERE, h_last=HERE + 1024), dict(y=HERE, h0=HERE, h_last=HERE),
+    dict(y=HERE, A=HERE), dict(y=HERE, dt_bias=HERE + 16), dict(y=HERE, slots=HERE + 64),
+    dict(y=HERE, cu_seqlens=HERE + 4), dict(h_last=HERE, q=HERE + 16), dict(h_last=HERE, beta=HERE + 64),
+    dict(h_last=HERE, h0=HERE, v=HERE), dict(h_last=HERE, slots=HERE + 8), dict(h_last=HERE + 16, A=HERE + 16),
+])
+def test_scan_rejects_overlap(lib, kw):
+    """Outputs on inputs or on one another; that h_last is h0 is no overlap."""
+    assert lib.gdr_chunk_scan_fwd(ctypes.byref(_scan(**kw)), None) == SHAPE
+
+
+@pytest.mark.parametrize("name", ["q", "v", "dt", "A", "y", "h0", "h_last", "cu_seqlens", "slots"])
+def test_scan_rejects_overlap_with_its_workspace(lib, name):
+    a = _scan(seqlen=640)
+    n = ctypes.c_size_t()
+    setattr(a, name, HERE + 4096)
+    assert lib.gdr_chunk_scan_workspace(ctypes.byref(a), ctypes.byref(n)) == OK
+    a.workspace, a.workspace_bytes = HERE, n.value
+    assert lib.gdr_chunk_scan_fwd(ctypes.byref(a), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=FAR + 16), dict(state_io=P), dict(state_io=P, y=HERE), dict(q=FAR + 4096), dict(beta=FAR + 64),
+    dict(A=FAR + 64), dict(dt_bias=FAR + (1 << 30) + 64), dict(slots=FAR + 4), dict(slots=FAR + (1 << 30)),
+])
+def test_step_rejects_overlap(lib, kw):
+    assert lib.gdr_scan_step(ctypes.byref(_step(**kw)), None) == SHAPE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(u=P + (1 << 20)), dict(u=P + (1 << 22)), dict(bias=FAR + 64), dict(slots=FAR + 4), dict(w=P + (1 << 21)),
+    dict(bias=P + (1 << 21)), dict(slots=P + (1 << 21) + 4), dict(cu_seqlens=P + (1 << 21)),
+])
+def test_conv_rejects_overlap(lib, kw):
+    assert lib.ssm_conv1d_packed_fwd(ctypes.byref(_conv(**kw)), None) == SHAPE
