@@ -549,6 +549,12 @@ def gdr_chunk_scan_fwd(q, k, v, dt, A, beta, dt_bias=None, h0=None, *, scale=Non
     _expect("h0", h0, torch.float32, (rows, h, K, V), dev)
     _expect("h_last", h_last, torch.float32, (rows, h, K, V), dev)
     _expect("y", y, v.dtype, (b, Lq, h, V), dev)
+    if workspace is not None:  # (device memory for host tensors too)
+        if not workspace.is_cuda or workspace.get_device() != (
+                dev if dev >= 0 else torch.cuda.current_device()):
+            raise ValueError("workspace is on %s, the call runs on %s" % (
+                workspace.device, "cuda:%d" % dev if dev >= 0 else "the current CUDA device"))
+        _own("workspace", workspace)
     host_y, host_h = y, h_last
     sg = None
     if not v.is_cuda:

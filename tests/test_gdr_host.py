@@ -268,3 +268,10 @@ def test_step_rejects_overlap(lib, kw):
 ])
 def test_conv_rejects_overlap(lib, kw):
     assert lib.ssm_conv1d_packed_fwd(ctypes.byref(_conv(**kw)), None) == SHAPE
+
+
+def test_binding_refuses_a_workspace_on_the_host():
+    d = I.gdr_inputs(1, 80, 1, 1, 64, 64, io="bf16")
+    for space in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="workspace"):
+            ops.gdr_chunk_scan_fwd(d["q"], d["k"], d["v"], d["dt"], d["A"], d["beta"], workspace=space)

@@ -812,3 +812,26 @@ def test_scan_few_long_strengths(cuda_ok, L, flags):
     ry, rh, _ = _ref(d, flags=flags)
     _close(y, ry, "y")
     _close(h, rh, "h_last")
+
+
+def test_scan_workspace_of_the_caller(cuda_ok):
+    """One that is large enough is used, a small one replaced; what is not the
+    memory it counts, or lies elsewhere, is refused before anything runs."""
+    ops = _ops()
+    d = _dev(I.gdr_inputs(1, 200, 1, 2, 64, 64, seed=16))
+    y0, h0 = _scan(d)
+    space = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    y, h = _scan(d, workspace=space)
+    assert torch.equal(y, y0) and torch.equal(h, h0) and (space != 0).any()
+    y, h = _scan(d, workspace=space[:64])
+    assert torch.equal(y, y0) and torch.equal(h, h0)
+    for bad in (space[:1].expand(1 << 20), space[::2], space.cpu()):
+        with pytest.raises(ValueError):
+            _scan(d, workspace=bad)
+    with pytest.raises(ops.L.SsmError):  # off 16 bytes
+        _scan(d, workspace=space[8:])
+    host = {k: None if x is None else x.cpu() for k, x in d.items()}
+    y, h = _scan(host, workspace=space)
+    assert torch.equal(y, y0.cpu()) and torch.equal(h, h0.cpu())
+    with pytest.raises(ValueError):
+        _scan(host, workspace=space.cpu())
