@@ -628,9 +628,10 @@ ssm_status_t gdr_gated_rmsnorm_fwd(const gdr_norm_args_t *args, void *stream);
  *
  * x, u: [tokens, channels] (io), `x_row` elements between x's rows (0 =
  * dense), u dense; w, bias, flags and the arithmetic as ssm_conv1d_fwd.
- *   cu_seqlens: [sequences + 1] int32, non-decreasing: sequence i is the rows
- *     cu_seqlens[i] .. cu_seqlens[i + 1].  Rows of no sequence are left as
- *     they were.  A pair outside 0 .. tokens is an empty sequence.
+ *   cu_seqlens: [sequences + 1] int32, as for gdr_chunk_scan_fwd: sequence i is
+ *     the rows cu_seqlens[i] .. cu_seqlens[i + 1].  Rows of no sequence are left
+ *     as they were.  A pair that is out of order or outside 0 .. tokens is an
+ *     empty sequence.
  *   state: [state_rows, channels, width - 1] float32 or NULL (zeros): the
  *     inputs before each sequence, oldest first, updated in place to the
  *     last width - 1 inputs (a decode batch is sequences of one token).

@@ -8,11 +8,12 @@
 //
 // Bound by its bytes.  A thread takes V consecutive channels over a run of RUN
 // tokens of one sequence, the W - 1 previous inputs in registers.  Runs are
-// numbered so that every sequence starts a run of its own without a scan over
-// the lengths: sequence i, from row s_i, has the runs floor(s_i / RUN) + i and
-// on, which leaves it at least ceil(len / RUN); a CTA's run is one, and each
-// warp looks for its sequence together.  The thread with a sequence's first
-// run is the only one that touches its state: it reads the old inputs, and
+// numbered without a scan over the lengths, whatever the order of the sequences:
+// sequence i's first run is tokens / RUN + i, and a later one, from row t, is
+// t / RUN - 1 (the RUN rows before it are its sequence's, so among sequences that
+// are apart no two later runs start within the same RUN rows); a CTA's run is one,
+// and each warp looks for its sequence together.  The thread with a sequence's
+// first run is the only one that touches its state: it reads the old inputs, and
 // takes the new ones from x, so no other thread's order matters and one launch
 // does.
 //
@@ -110,26 +111,27 @@ template <int N> __device__ __forceinline__ void store_floats(float *p, const fl
   }
 }
 
-// Whether run `run` is one of sequence i's (a valid pair of bounds, a slot that
-// is not padding).
+// Whether run `run` is one of sequence i's behind its first (a valid pair of
+// bounds, a slot that is not padding).
 template <int RUN>
 __device__ __forceinline__ bool has_run(const ConvPackedParams &p, int64_t i, int64_t run) {
-  const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / RUN + i;
+  const int64_t b = p.cu[i], e = p.cu[i + 1], first = b / RUN;
   const int64_t slot = p.slots ? (int64_t)p.slots[i] : 0;
-  return b >= 0 && e > b && e <= p.tokens && first <= run && run < first + (e - b + RUN - 1) / RUN &&
+  return b >= 0 && e > b && e <= p.tokens && first <= run && run < first + (e - b - 1) / RUN &&
          (!p.slots || (slot >= 0 && slot < p.state_rows));
 }
 
-// The sequence with run `run`, by a whole warp (-1: none).  The last whose first
-// run is not after it has it where the bounds do not decrease: among up to 1024
-// by counting (one round of loads), among more by bisection.  Where it does not,
-// the up to 1024 are looked through.
+// The sequence with run `run`, by a whole warp (-1: none).  Of a later run the last
+// that does not start behind the RUN rows before it has it where the bounds do not
+// decrease: among up to 1024 by counting (one round of loads), among more by
+// bisection.  Where it does not, the up to 1024 are looked through.
 template <int RUN>
 __device__ __forceinline__ int64_t find_sequence(const ConvPackedParams &p, int64_t run) {
+  if (run >= p.tokens / RUN) return run - p.tokens / RUN;
   if (p.nseq <= 1024) {
     const int lane = threadIdx.x & 31;
     int n = 0;
-    for (int i = lane; i < (int)p.nseq; i += 32) n += (int64_t)p.cu[i] / RUN + i <= run;
+    for (int i = lane; i < (int)p.nseq; i += 32) n += p.cu[i] / RUN <= run;
     n = __reduce_add_sync(0xffffffffu, n);
     if (n > 0 && has_run<RUN>(p, n - 1, run)) return n - 1;
     int at = -1;
@@ -140,10 +142,10 @@ __device__ __forceinline__ int64_t find_sequence(const ConvPackedParams &p, int6
   int64_t lo = 0, hi = p.nseq - 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
-    if ((int64_t)p.cu[mid] / RUN + mid <= run) lo = mid;
+    if (p.cu[mid] / RUN <= run) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  return p.cu[lo] / RUN <= run ? lo : -1;
 }
 
 template <int BYTES> __device__ __forceinline__ void cp_async(void *dst, const void *src) {
@@ -190,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, RUN == kShort ? 8 : 1) conv1d_packed
   const int64_t seq = find_sequence<RUN>(p, run);
   if (!mine || seq < 0) return;
   const int64_t begin = p.cu[seq], end = p.cu[seq + 1];
-  const int64_t j = run - (begin / RUN + seq);
-  if (begin < 0 || end < begin || end > p.tokens || j < 0) return;
+  if (begin < 0 || end < begin || end > p.tokens) return;
+  const int64_t j = run >= p.tokens / RUN ? 0 : run - begin / RUN + 1;
   const int64_t slot = p.slots ? (int64_t)p.slots[seq] : seq;
   if (p.slots && (slot < 0 || slot >= p.state_rows)) return;
   const int64_t t0 = begin + j * RUN;

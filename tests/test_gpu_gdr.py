@@ -835,3 +835,32 @@ def test_scan_workspace_of_the_caller(cuda_ok):
     assert torch.equal(y, y0.cpu()) and torch.equal(h, h0.cpu())
     with pytest.raises(ValueError):
         _scan(host, workspace=space.cpu())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C", [(1024, 64), (1024, 5), (60, 64), (60, 5)])
+def test_conv_packed_bounds_going_back(cuda_ok, rows, C, io):
+    """As test_scan_bounds_going_back, in both forms (few sequences, and many
+    for their rows)."""
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[io]
+    g = torch.Generator().manual_seed(rows + C)
+    x = torch.randn(rows, C, generator=g).to(dtype)
+    w, bias = torch.randn(C, 4, generator=g), torch.randn(C, generator=g)
+    sets = [s for s in _sets_going_back(rows, 60, seed=C) if max(s) <= rows]
+    assert any(rows < 16 * (len(s) - 1) for s in sets) == (rows == 60)
+    for bounds in sets:
+        n = len(bounds) - 1
+        state = torch.randn(n, C, 3, generator=g)
+        u = torch.full((rows, C), 7.0, dtype=dtype).cuda()
+        got = state.cuda()
+        _ops().ssm_conv1d_packed_fwd(x.cuda(), w.cuda(), bias.cuda(), got, u=u,
+                                     cu_seqlens=torch.tensor(bounds, dtype=torch.int32, device="cuda"))
+        rest = torch.ones(rows, dtype=torch.bool)
+        want = state.double().numpy()
+        for i, b, e in _apart(bounds, rows):
+            ru, rs = O.conv1d_packed(x[b:e], w, bias, state[i:i + 1], [e - b])
+            _close(u[b:e], ru, "u %s %d" % (bounds, i))
+            want[i] = rs[0]
+            rest[b:e] = False
+        assert np.array_equal(_np(got), want), bounds
+        assert (u[rest.cuda()] == 7).all(), bounds
