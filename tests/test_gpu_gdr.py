@@ -864,3 +864,57 @@ def test_conv_packed_bounds_going_back(cuda_ok, rows, C, io):
             rest[b:e] = False
         assert np.array_equal(_np(got), want), bounds
         assert (u[rest.cuda()] == 7).all(), bounds
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("W", [1, 2, 3, 4])
+@pytest.mark.parametrize("C", [64, 12, 331])
+def test_conv_packed_short_runs(cuda_ok, C, W, io):
+    """The form for sequences that are short on average: some of several of its
+    runs among them, histories and states from x, from the old state and both."""
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16}[io]
+    lengths = [1, 7, 8, 9, 17, 33, 0, 1, 2, 3, 1, 1, 2, 16, 64, 3] + [1, 2, 3, 0] * 8
+    total, n = sum(lengths), len(lengths)
+    assert total + 5 < 16 * n
+    g = torch.Generator().manual_seed(C + W)
+    wide = torch.randn(total + 5, C + 8, generator=g).to(dtype)
+    wide[total:] = float("nan")
+    w, bias = torch.randn(C, W, generator=g), torch.randn(C, generator=g)
+    cache = torch.randn(n + 3, C, W - 1, generator=g)
+    slots = torch.randperm(n + 3, generator=g)[:n].to(torch.int32)
+    skip = [4, 20]
+    index = slots.clone()
+    index[skip[0]], index[skip[1]] = -1, n + 3
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32)
+    u = torch.full((total + 5, C), 7.0, dtype=dtype).cuda()
+    got = cache.cuda()
+    _ops().ssm_conv1d_packed_fwd(wide.cuda()[:, :C], w.cuda(), bias.cuda(), got, cu_seqlens=cu.cuda(),
+                                 slots=index.cuda(), u=u)
+    ru, rs = O.conv1d_packed(wide[:total, :C], w, bias, cache[slots.long()], lengths)
+    live = torch.cat([torch.full((m,), i not in skip) for i, m in enumerate(lengths)])
+    # float32: W + 3 roundings; bfloat16: its rounding and the hardware tanh
+    _close(u[:total][live.cuda()], ru[live.numpy()], "u")
+    assert (u[:total][~live.cuda()] == 7).all() and (u[total:] == 7).all()
+    on = [i for i in range(n) if i not in skip]
+    assert torch.equal(got.cpu()[slots.long()[on]].double(), torch.from_numpy(rs).reshape(n, C, W - 1)[on])
+    rest = [i for i in range(n + 3) if i not in slots[on].tolist()]
+    assert torch.equal(got.cpu()[rest], cache[rest])
+
+
+@pytest.mark.parametrize("long", [1, 40000])
+@pytest.mark.parametrize("C", [64, 13])
+def test_conv_packed_many(cuda_ok, C, long):
+    """More sequences than are looked through, in both forms."""
+    g = torch.Generator().manual_seed(C)
+    n = 1500
+    lengths = (torch.rand(n, generator=g) * 4).int().tolist()
+    lengths[5], lengths[n - 3] = 150, long
+    total = sum(lengths)
+    assert (total < 16 * n) == (long == 1)
+    x, w, state = torch.randn(total, C, generator=g), torch.randn(C, 4, generator=g), torch.randn(n, C, 3, generator=g)
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
+    got = state.cuda()
+    u, _ = _ops().ssm_conv1d_packed_fwd(x.cuda(), w.cuda(), None, got, cu_seqlens=cu)
+    ru, rs = O.conv1d_packed(x, w, None, state, lengths)
+    _close(u, ru, "u")
+    assert torch.equal(got.cpu().double(), torch.from_numpy(rs))
