@@ -708,8 +708,11 @@ __global__ void __launch_bounds__(kPrepThreads, 6)
       __syncthreads();  // T takes A's place
       // (a bound of the rows' sums: the largest of each half)
       const float tn = fmaxf(s.tn[0], s.tn[1]) + fmaxf(s.tn[2], s.tn[3]);
+      // T goes as it is where its digits and range are float16's (the second kernel
+      // need not take a scale back), by a power of two where it is larger or, as
+      // strengths below 1/16 make it, smaller
       int eT = scale_exp(tn);
-      eT = eT < 0 ? eT : 0;
+      eT = eT < 0 || tn < 0.0625f ? eT : 0;
       const f2 sc = mk2(pow2i(eT), pow2i(eT));
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -1342,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           nb[2 * q + 1] = mul2(mk2(cu.z, cu.w), fU);
         }
       }
-      const float un = pow2i(-eT);  // 1 but for very large T
+      const float un = pow2i(-eT);  // 1 but for very large or small T
       // U and U'
       wait(&s.udone, ph, 15);
       tc_fence_after();

@@ -918,3 +918,19 @@ def test_conv_packed_many(cuda_ok, C, long):
     ru, rs = O.conv1d_packed(x, w, None, state, lengths)
     _close(u, ru, "u")
     assert torch.equal(got.cpu().double(), torch.from_numpy(rs))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("raw", [False, True])
+def test_scan_small_strengths(cuda_ok, raw, io):
+    """Write strengths of some 4e-5 throughout: the state, small beside the
+    values, keeps its digits."""
+    d = I.gdr_inputs(1, 200, 1, 2, 128, 64, io=io, seed=17)
+    d["beta"] = d["beta"] - 10
+    if raw:
+        d["beta"] = d["beta"].float().sigmoid().to(d["beta"].dtype)
+    flags = 17 if raw else 25
+    y, h = _scan(_dev(d), flags=flags)
+    ry, rh, _ = _ref(d, flags=flags)
+    _close(y, ry, "y")
+    _close(h, rh, "h_last")
