@@ -1429,7 +1429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The state entering segment i + 1 from the one entering segment i: S <- M S +
 // N, N the segment's own state from zeros (in the place of the result), M its
 // map.  One CTA per (sequence, head, 16 value columns), over the segments in
-// turn, a warp 16 key rows; the products as float32 on mma.  A lane takes four
+// turn, a warp 16 key rows; the products as float32 on mma, each step's summed by
+// itself and added with rounding (mma's own sums are cut off, which without decay,
+// where most of M is 1 on the diagonal, came to 2e-5 of the state).  A lane takes four
 // neighbouring columns of M for the four k of two steps (the sum's order is
 // free), so M comes in 16-byte loads, the next segment's under this one's.
 constexpr int kCarryCols = 16, kCarryRow = 18;  // (18: no bank conflicts)
@@ -1500,9 +1502,12 @@ __global__ void __launch_bounds__(256) gdr_carry_kernel(const GdrTcParams tp) {
           uint32_t bh[2], bl[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) split_tf32(buf[16 * b + 4 * t + 2 * h + e][8 * n + r], bh[e], bl[e]);
-          mma_tf32(c[n], al, bh);
-          mma_tf32(c[n], ah, bl);
-          mma_tf32(c[n], ah, bh);
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_tf32(d, al, bh);
+          mma_tf32(d, ah, bl);
+          mma_tf32(d, ah, bh);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[n][e] += d[e];
         }
       }
     }

@@ -934,3 +934,17 @@ def test_scan_small_strengths(cuda_ok, raw, io):
     ry, rh, _ = _ref(d, flags=flags)
     _close(y, ry, "y")
     _close(h, rh, "h_last")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("L,K", [(1829, 128), (6000, 64)])
+def test_scan_few_long_untouched(cuda_ok, L, K, io):
+    """Without decay, under one key: what the entering state holds beside it is
+    handed from segment to segment as it is."""
+    d = I.gdr_inputs(2, L, 1, 1, K, 64, io=io, seed=18, h0=True)
+    d["dt"] = None
+    d["k"][:] = d["k"][:, :1]
+    y, h = _scan(_dev(d))
+    ry, rh, _ = _ref(d)
+    _close(y, ry, "y")
+    _close(h, rh, "h_last")
