@@ -293,7 +293,7 @@ __device__ __forceinline__ void put_product(float *o, const float (&c)[MT][4], f
 // substitution, a column a lane; then twice -T22 A21 T11 for the block below two
 // of them, the products as float32 on mma (a multiply-add version read its
 // operands from shared memory four times as often, which bound the kernel: 4200
-// cycles a unit of SM time).  Bound by issue: 8500 warp instructions a unit, half
+// cycles a unit of SM time).  Bound by issue: 8700 warp instructions a unit, half
 // of the slots taken; barriers and instruction fetch are the largest stalls.
 template <int KD>
 __global__ void __launch_bounds__(kPrepThreads, 6)

@@ -26,6 +26,7 @@ template <> struct V16<__nv_bfloat16> {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
   }
+  // (z / (1 + e^-z) keeps the digits of small values: 16384 x 32 rows of 128 76 us, this 73)
   static __device__ __forceinline__ float gate(float z) { return silu_tanh(z); }
 };
 template <> struct V16<float> {
